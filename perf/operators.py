@@ -61,7 +61,8 @@ def draw(rng):
         return {"op": op, "T": T, "H": 32 * _log(rng, 1, 128), "fmt": rng.choice(["e2m1", "e4m3"]), "skip": rng.choice([0, 8, 64])}
     if op == "gemm":
         a, w = rng.choice([("e2m1", "e2m1"), ("e4m3", "e2m1"), ("e4m3", "e4m3")])
-        return {"op": op, "T": T, "N": _log(rng, 1, 4096), "K": 32 * _log(rng, 1, 128), "a": a, "w": w, "out": rng.choice(["bf16", "bf16", "f32"])}
+        return {"op": op, "T": T, "N": _log(rng, 1, 4096), "K": 32 * _log(rng, 1, 128), "a": a, "w": w,
+                "out": rng.choice(["bf16", "f32"]) if a == "e2m1" else "bf16"}   # fp32 outputs are the 4-bit product's alone
     E, dtype = rng.choice([8, 64, 128]), rng.choice(["bf16", "bf16", "f32"])
     return {"op": op, "way": rng.choice(["forward", "backward"]), "T": T, "H": 8 * _log(rng, 8, 512 if dtype == "bf16" else 256), "E": E,
             "local": rng.choice([E, E, E // 2]), "K": rng.randint(1, 8), "tile": rng.choice([16, 32, 64, 128]),
