@@ -488,6 +488,119 @@ int moe_finalize(const uint16_t* rows, int64_t rows_stride, int n_partials,
                  const uint16_t* norm_weight, float gain_center, float eps,
                  int weight_before_norm, int T, int K, int H, uint16_t* out, void* stream);
 
+/* ------------------------------------------------------------------ MX formats
+ * OCP microscaling: 32 consecutive elements of a row under one e8m0 scale byte
+ * b of value 2^(b - 127) (255: NaN), the elements e2m1 (two codes a byte,
+ * element 2j in the low nibble of byte j) or e4m3 (one byte each). The dense
+ * products around the experts (the model page, "MuseSpark1xMoE": the pooler and
+ * unpooler projections) in these formats, with the quantizer of their left
+ * operand alone and inside the residual norm in front of them.
+ *
+ * Of a block with largest magnitude m (emax = 2 for e2m1, 8 for e4m3):
+ *   b = max(0, floor(log2 m) + 127 - emax), 0 for m = 0
+ *   code_i = v_i * 2^(127 - b) to nearest even, saturating at 6 or 448; the sign
+ *            bit follows v_i
+ *   any NaN or infinity in the block: b = 255, codes 0 */
+#define MOE_MX_E2M1 0
+#define MOE_MX_E4M3 1
+
+/* element types of rows and outputs */
+#define MOE_BF16 0
+#define MOE_F32 1
+
+#define MOE_MAX_MX_K (1 << 20) /* K of mx_gemm */
+
+/* x -> codes and scales.
+ *   x      device bf16 [T, H], row stride x_row_stride elements (>= H, % 8 == 0)
+ *   codes  device uint8 [T, H/2] (e2m1) or [T, H] (e4m3) out
+ *   sf     device uint8 [T, H/32] out
+ * H % 32 == 0. One launch on `stream`. */
+int mx_quant(const uint16_t* x, int64_t x_row_stride, int T, int H, int fmt, uint8_t* codes, uint8_t* sf,
+             void* stream);
+
+/* code * 2^(b - 127), rounded once to bf16 (nearest even; exact unless the
+ * value leaves bf16's range: infinity, or its subnormals); NaN under scale 255
+ * and for the e4m3 NaN codes. Shapes as mx_quant; out has row stride
+ * out_row_stride elements (>= H, % 8 == 0). */
+int mx_dequant(const uint8_t* codes, const uint8_t* sf, int T, int H, int fmt, uint16_t* out,
+               int64_t out_row_stride, void* stream);
+
+/* The residual's addition, the RMSNorm of the sum, and its MX codes, in one
+ * pass (the model page, "MuseSpark1xDecoderLayer": a residual boundary; the
+ * norm's arithmetic is nvfp4_norm_quant's). Per row of H values:
+ *   h_j = bf16(x_j + residual_j)      (the fp32 sum, rounded; h = x with no residual)
+ *   s   = sum_j h_j^2 in fp64;  ms = fp32(s / H);  r = 1 / sqrt(ms + eps)
+ *   y_j = (h_j * r) * gamma_j,  gamma_j = fp32(norm_weight_j) + gain_center
+ *   y -> MX codes and scales (a row that holds a NaN or an infinity: every block NaN)
+ *   x            device bf16 [T, H], row stride x_row_stride elements
+ *   residual     device bf16 [T, H], or NULL
+ *   norm_weight  device bf16 [H], or NULL (ones)
+ *   sum          device bf16 [T, H] out: h. It may be `residual` or `x` itself (with its
+ *                row stride), no other overlap; NULL only without a residual
+ *   codes, sf    as mx_quant
+ * H % 32 == 0, H <= MOE_MAX_HIDDEN, eps in (0, 1], row strides >= H and % 8 == 0.
+ * One launch on `stream`. */
+int mx_add_norm_quant(const uint16_t* x, int64_t x_row_stride, const uint16_t* residual,
+                      int64_t residual_row_stride, const uint16_t* norm_weight, float gain_center, float eps,
+                      int T, int H, int fmt, uint16_t* sum, int64_t sum_row_stride, uint8_t* codes, uint8_t* sf,
+                      void* stream);
+
+/* out[t, n] = sum_k a[t, k] * w[n, k] over the dequantized values, in fp32
+ * accumulators, rounded once to out's type.
+ *   a_codes, a_sf  device: MX [T, K], a_fmt
+ *   w_codes, w_sf  device: MX [N, K], w_fmt (row-major, as mx_quant writes)
+ *   out            device [T, N], row stride out_row_stride elements (>= N), of
+ *                  type out_dtype: MOE_BF16, or MOE_F32 where both operands are e2m1
+ * (a_fmt, w_fmt): (e2m1, e2m1), (e4m3, e2m1) or (e4m3, e4m3). The sum of e2m1
+ * products is exact to fp32; where an operand is e4m3 the matrix cores cut each
+ * product to 13 bits below the exponent of the largest of its 8, about 1.5e-5 of
+ * the result. A NaN
+ * scale makes the row or column NaN. K % 32 == 0, K <= MOE_MAX_MX_K; any T and
+ * N. One launch on `stream`, no workspace. */
+int mx_gemm(const uint8_t* a_codes, const uint8_t* a_sf, int a_fmt, const uint8_t* w_codes, const uint8_t* w_sf,
+            int w_fmt, int T, int N, int K, void* out, int64_t out_row_stride, int out_dtype, void* stream);
+
+/* ------------------------------------------------------------------ tokens by expert and back
+ * The sort of tokens by expert on moe_route's maps, and back with the routes'
+ * weights applied, with the gradients of both, for experts (or their backward
+ * pass) that a caller runs by itself; moe_experts_fwd gathers its rows itself.
+ * p(t,k) = exp2perm[t*K + k]; routes with p = -1 take no part.
+ *   exp2perm    device int32 [T, K], perm2tok device int32 [rows_max],
+ *   total_rows  device int32 [1] (4-byte aligned): the fields of that name in
+ *               moe_route's metadata; no row is the target of two routes
+ * Padding rows (perm2tok = -1) below total_rows are written as zeros where rows
+ * are written; rows from total_rows on are left as they were. Every sum has a
+ * fixed order: results do not change from call to call. Row strides count
+ * elements and are >= H and % 8 == 0 (moe_dispatch: bytes, >= row_bytes, % 16 == 0).
+ * dtype: MOE_BF16 or MOE_F32, of rows and token rows alike. One launch each.
+ *
+ * moe_dispatch: rows[p(t,k)] = x[t], rows of any type as bytes (quantized codes
+ * and scales too); row_bytes % 16 == 0, at most 4 * MOE_MAX_HIDDEN. */
+int moe_dispatch(const void* x, int64_t x_row_stride_bytes, int64_t row_bytes, const int32_t* exp2perm,
+                 const int32_t* perm2tok, const int32_t* total_rows, int T, int K, int64_t rows_max, void* rows,
+                 int64_t rows_stride_bytes, void* stream);
+
+/* moe_dispatch's gradient: d_x[t] = sum_k d_rows[p(t,k)], k ascending in fp32,
+ * rounded once. H % 8 == 0, H <= MOE_MAX_HIDDEN (here and below). */
+int moe_dispatch_bwd(const void* d_rows, int64_t rows_stride, int dtype, const int32_t* exp2perm, int T, int K,
+                     int64_t rows_max, int H, void* d_x, int64_t d_x_row_stride, void* stream);
+
+/* out[t] = sum_k topk_weights[t, k] * rows[p(t,k)], k ascending in fp32, rounded
+ * once. topk_weights: device fp32 [T, K]. */
+int moe_combine(const void* rows, int64_t rows_stride, int dtype, const int32_t* exp2perm,
+                const float* topk_weights, int T, int K, int64_t rows_max, int H, void* out,
+                int64_t out_row_stride, void* stream);
+
+/* moe_combine's gradients:
+ *   d_rows[p(t,k)]  = topk_weights[t, k] * d_out[t], rounded once
+ *   d_weights[t, k] = sum_j rows[p(t,k), j] * d_out[t, j] in fp32; 0 where p(t,k) = -1
+ * d_rows [rows_max, H] may be `rows` itself (with its row stride), no other
+ * overlap; d_weights device fp32 [T, K]. */
+int moe_combine_bwd(const void* d_out, int64_t d_out_row_stride, const void* rows, int64_t rows_stride, int dtype,
+                    const int32_t* exp2perm, const int32_t* perm2tok, const int32_t* total_rows,
+                    const float* topk_weights, int T, int K, int64_t rows_max, int H, void* d_rows,
+                    int64_t d_rows_stride, float* d_weights, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

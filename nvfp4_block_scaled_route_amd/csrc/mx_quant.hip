@@ -1,0 +1,275 @@
+// The MX quantizer, its inverse, and the residual addition with RMSNorm whose
+// output is MX: the activations of the dense products around the experts (the
+// model page, "MuseSpark1xMoE": the pooler and unpooler projections; the
+// residual boundary in front of them), in OCP microscaling formats.
+//
+//   mx_quant           x -> codes, e8m0 scales (per 32 values)
+//   mx_dequant         codes, scales -> bf16 values
+//   mx_add_norm_quant  h = bf16(x + residual); y = h / rms(h) * gain; MX(y)
+//
+// All three are HBM-bound and read and write each byte once. A lane owns 8
+// values (one 16-byte bf16 load; 8 or 4 code bytes out), a quad one block: its
+// amax is two DPP steps over the magnitudes' bits, no LDS.
+#include "mx.hpp"
+
+namespace moe {
+
+constexpr int kMqThreads = 256;
+
+struct MqArgs {
+    const uint16_t* x;
+    int64_t x_row_stride;
+    int64_t octs;           // T * H / 8
+    int row_octs;           // H / 8
+    uint8_t* codes;
+    uint8_t* sf;
+};
+
+// Octet `first + tid` of the T x H values, row by row: a workgroup finds the
+// row of its first octet once (a uniform 64-bit division), a lane its own by a
+// 32-bit one. first is a multiple of 4 and H of 32, so quads hold whole blocks.
+template <int FMT>
+__global__ void __launch_bounds__(kMqThreads) mx_quant_kernel(MqArgs a) {
+    const int64_t first = (int64_t)blockIdx.x * kMqThreads;
+    const int64_t row0 = first / a.row_octs;
+    const uint32_t off = (uint32_t)(first - row0 * a.row_octs) + threadIdx.x;
+    if (first + threadIdx.x >= a.octs) return;
+    const uint32_t dr = off / (uint32_t)a.row_octs;
+    const int oct = (int)(off - dr * (uint32_t)a.row_octs);
+    const int64_t t = row0 + dr;
+    float v[8];
+    unpack8(*reinterpret_cast<const uint4*>(a.x + t * a.x_row_stride + (int64_t)oct * 8), v);
+    mx_store8<FMT>(v, oct, a.codes + t * mx_bytes((int64_t)a.row_octs * 8, FMT), a.sf + t * (a.row_octs >> 2));
+}
+
+struct MdArgs {
+    const uint8_t* codes;
+    const uint8_t* sf;
+    int64_t octs;
+    int row_octs;
+    uint16_t* out;
+    int64_t out_row_stride;
+};
+
+// code * 2^(byte - 127) in fp32 (exact but below 2^-149; the factor of byte 0
+// is the subnormal 2^-127), rounded once to bf16; NaN under byte 255.
+template <int FMT>
+__global__ void __launch_bounds__(kMqThreads) mx_dequant_kernel(MdArgs a) {
+    const int64_t first = (int64_t)blockIdx.x * kMqThreads;
+    const int64_t row0 = first / a.row_octs;
+    const uint32_t off = (uint32_t)(first - row0 * a.row_octs) + threadIdx.x;
+    if (first + threadIdx.x >= a.octs) return;
+    const uint32_t dr = off / (uint32_t)a.row_octs;
+    const int oct = (int)(off - dr * (uint32_t)a.row_octs);
+    const int64_t t = row0 + dr, i = first + threadIdx.x;
+    const uint32_t byte = a.sf[i >> 2];
+    const float s = byte == 255u ? __uint_as_float(0x7FC00000u)
+                                 : byte == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23);
+    float v[8];
+    if constexpr (FMT == MOE_MX_E2M1) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(a.codes + i * 4);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {   // magnitude codes 0 .. 7: 0, .5, 1, 1.5, 2, 3, 4, 6
+            const uint32_t c = (w >> (4 * k)) & 15u, e = (c >> 1) & 3u, m = c & 1u;
+            const float mag = e == 0u ? 0.5f * (float)m : __uint_as_float(((e + 126u) << 23) | (m << 22));
+            v[k] = (c & 8u) ? -mag : mag;
+        }
+    } else {
+        const uint2 w = *reinterpret_cast<const uint2*>(a.codes + i * 8);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t c = ((k < 4 ? w.x : w.y) >> (8 * (k & 3))) & 255u;
+            v[k] = (c & 127u) == 127u ? __uint_as_float(0x7FC00000u) : e4m3_decode(c);
+        }
+    }
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        o[k] = f32_to_bf16(__fmul_rn(v[2 * k], s)) | (f32_to_bf16(__fmul_rn(v[2 * k + 1], s)) << 16);
+    *reinterpret_cast<uint4*>(a.out + t * a.out_row_stride + (int64_t)oct * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// ------------------------------------------------------------------ residual + norm + MX
+struct AnArgs {
+    const uint16_t* x;
+    int64_t x_row_stride;
+    const uint16_t* residual;       // or NULL
+    int64_t residual_row_stride;
+    const uint16_t* norm_weight;    // or NULL: ones
+    float gain_center, eps;
+    int T, H;
+    uint16_t* sum;                  // or NULL (no residual)
+    int64_t sum_row_stride;
+    uint8_t* codes;
+    uint8_t* sf;
+};
+
+__device__ __forceinline__ double wave_sum_d(double v) {
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
+    return v;
+}
+
+// A row is held by W waves (W = 1: four rows a workgroup; else one), NB octets
+// a lane, in registers from the load to the codes: one pass over memory. The
+// sum of squares is formed in fp64 (each square exact) and rounded once.
+//   * many rows: one wave a row, no barrier;
+//   * few rows, or rows above 4096 values: a workgroup of 256 to 1024 threads a
+//     row, so that a single token's row is in flight at once.
+template <int FMT, int NB, bool WIDE>
+__global__ void __launch_bounds__(WIDE ? 1024 : 256) add_norm_kernel(AnArgs a) {
+    __shared__ double s_part[16];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t t = WIDE ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + wave;
+    if (!WIDE && t >= a.T) return;
+    const int first = WIDE ? threadIdx.x : lane, step = WIDE ? blockDim.x : 64;
+    const int row_octs = a.H >> 3;
+    uint4 h[NB], r[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+        const int o = first + i * step;
+        h[i] = r[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (o < row_octs) {
+            h[i] = *reinterpret_cast<const uint4*>(a.x + t * a.x_row_stride + (int64_t)o * 8);
+            if (a.residual)
+                r[i] = *reinterpret_cast<const uint4*>(a.residual + t * a.residual_row_stride + (int64_t)o * 8);
+        }
+    }
+    double ss = 0.0;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+        const int o = first + i * step;
+        if (o >= row_octs) continue;
+        float v[8], w[8];
+        unpack8(h[i], v);
+        if (a.residual) {
+            // the fp32 sum rounded to bf16, the residual stream's type: the norm
+            // is of the values that the next layer will read
+            unpack8(r[i], w);
+            uint32_t b[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                b[k] = f32_to_bf16(__fadd_rn(v[k], w[k]));
+                v[k] = bf16_to_f32(b[k]);
+            }
+            h[i] = make_uint4(b[0] | (b[1] << 16), b[2] | (b[3] << 16), b[4] | (b[5] << 16), b[6] | (b[7] << 16));
+        }
+        if (a.sum) *reinterpret_cast<uint4*>(a.sum + t * a.sum_row_stride + (int64_t)o * 8) = h[i];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) ss = __fma_rn((double)v[k], (double)v[k], ss);
+    }
+    ss = wave_sum_d(ss);
+    if constexpr (WIDE) {
+        if (lane == 0) s_part[wave] = ss;
+        __syncthreads();
+        ss = 0.0;
+        for (int w = 0; w < (int)(blockDim.x >> 6); ++w) ss += s_part[w];
+    }
+    const float ms = __double2float_rn(__ddiv_rn(ss, (double)a.H));
+    // sqrtf, not __fsqrt_rn: the latter is the bare v_sqrt_f32 here, which is off
+    // by an ulp now and then
+    const float rr = __fdiv_rn(1.0f, sqrtf(__fadd_rn(ms, a.eps)));
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+        const int o = first + i * step;
+        if (o >= row_octs) continue;
+        float v[8], g[8];
+        unpack8(h[i], v);
+        if (a.norm_weight) unpack8(*reinterpret_cast<const uint4*>(a.norm_weight + (int64_t)o * 8), g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            v[k] = __fmul_rn(__fmul_rn(v[k], rr), __fadd_rn(a.norm_weight ? g[k] : 1.0f, a.gain_center));
+        mx_store8<FMT>(v, o, a.codes + t * mx_bytes(a.H, FMT), a.sf + t * (a.H >> 5));
+    }
+}
+
+template <int FMT>
+void launch_add_norm(const AnArgs& a, hipStream_t s) {
+    // One wave a row from 1024 rows on (four waves a CU); below, the row is
+    // split over a workgroup.
+    if (a.T >= 1024 && a.H <= 4096) {
+        const dim3 g((unsigned)((a.T + 3) / 4)), b(256);
+        if (a.H <= 1024) hipLaunchKernelGGL((add_norm_kernel<FMT, 2, false>), g, b, 0, s, a);
+        else if (a.H <= 2048) hipLaunchKernelGGL((add_norm_kernel<FMT, 4, false>), g, b, 0, s, a);
+        else hipLaunchKernelGGL((add_norm_kernel<FMT, 8, false>), g, b, 0, s, a);
+        return;
+    }
+    const int octs = a.H >> 3;
+    int threads = (octs + 63) / 64 * 64;
+    if (threads > 1024) threads = 1024;
+    const dim3 g((unsigned)a.T), b((unsigned)threads);
+    if (octs <= 1024) hipLaunchKernelGGL((add_norm_kernel<FMT, 1, true>), g, b, 0, s, a);
+    else hipLaunchKernelGGL((add_norm_kernel<FMT, 2, true>), g, b, 0, s, a);
+}
+
+// Sizes, format, alignment and strides of an MX conversion between [T, H] bf16
+// rows and codes and scales.
+static int mx_check(const void* x, int64_t x_row_stride, int T, int H, int fmt, const void* codes, const void* sf,
+                    const char* name) {
+    if (T < 0 || H < 0) return fail(MOE_EINVAL, "%s: negative size T=%d H=%d", name, T, H);
+    if (!mx_fmt_ok(fmt)) return fail(MOE_EINVAL, "%s: format %d is neither MOE_MX_E2M1 nor MOE_MX_E4M3", name, fmt);
+    if (H % kMxBlock) return fail(MOE_EUNSUPPORTED, "%s: H=%d is not a multiple of 32", name, H);
+    if (T == 0 || H == 0) return MOE_OK;
+    if (!x || !codes || !sf) return fail(MOE_EINVAL, "%s: NULL pointer", name);
+    if (!aligned16(x) || !aligned16(codes) || !aligned16(sf))
+        return fail(MOE_EINVAL, "%s: pointers must be 16-byte aligned", name);
+    if (x_row_stride < H || x_row_stride % 8)
+        return fail(MOE_EINVAL, "%s: row stride %lld must be >= H and a multiple of 8", name, (long long)x_row_stride);
+    if (((int64_t)T * (H / 8) + kMqThreads - 1) / kMqThreads > 0x7FFFFFFF)
+        return fail(MOE_EUNSUPPORTED, "%s: too large", name);
+    return MOE_OK;
+}
+
+}  // namespace moe
+
+extern "C" int mx_quant(const uint16_t* x, int64_t x_row_stride, int T, int H, int fmt, uint8_t* codes, uint8_t* sf,
+                        void* stream) {
+    using namespace moe;
+    const int rc = mx_check(x, x_row_stride, T, H, fmt, codes, sf, "mx_quant");
+    if (rc != MOE_OK || T == 0 || H == 0) return rc;
+    MqArgs a{x, x_row_stride, (int64_t)T * (H / 8), H / 8, codes, sf};
+    const dim3 g((unsigned)((a.octs + kMqThreads - 1) / kMqThreads)), b(kMqThreads);
+    if (fmt == MOE_MX_E2M1) hipLaunchKernelGGL(mx_quant_kernel<MOE_MX_E2M1>, g, b, 0, (hipStream_t)stream, a);
+    else hipLaunchKernelGGL(mx_quant_kernel<MOE_MX_E4M3>, g, b, 0, (hipStream_t)stream, a);
+    return check_launch("mx_quant");
+}
+
+extern "C" int mx_dequant(const uint8_t* codes, const uint8_t* sf, int T, int H, int fmt, uint16_t* out,
+                          int64_t out_row_stride, void* stream) {
+    using namespace moe;
+    const int rc = mx_check(out, out_row_stride, T, H, fmt, codes, sf, "mx_dequant");
+    if (rc != MOE_OK || T == 0 || H == 0) return rc;
+    MdArgs a{codes, sf, (int64_t)T * (H / 8), H / 8, out, out_row_stride};
+    const dim3 g((unsigned)((a.octs + kMqThreads - 1) / kMqThreads)), b(kMqThreads);
+    if (fmt == MOE_MX_E2M1) hipLaunchKernelGGL(mx_dequant_kernel<MOE_MX_E2M1>, g, b, 0, (hipStream_t)stream, a);
+    else hipLaunchKernelGGL(mx_dequant_kernel<MOE_MX_E4M3>, g, b, 0, (hipStream_t)stream, a);
+    return check_launch("mx_dequant");
+}
+
+extern "C" int mx_add_norm_quant(const uint16_t* x, int64_t x_row_stride, const uint16_t* residual,
+                                 int64_t residual_row_stride, const uint16_t* norm_weight, float gain_center,
+                                 float eps, int T, int H, int fmt, uint16_t* sum, int64_t sum_row_stride,
+                                 uint8_t* codes, uint8_t* sf, void* stream) {
+    using namespace moe;
+    const char* name = "mx_add_norm_quant";
+    const int rc = mx_check(x, x_row_stride, T, H, fmt, codes, sf, name);
+    if (rc != MOE_OK) return rc;
+    if (H > MOE_MAX_HIDDEN) return fail(MOE_EUNSUPPORTED, "%s: H=%d above %d", name, H, MOE_MAX_HIDDEN);
+    if (!(eps > 0.0f) || eps > 1.0f || !(gain_center == gain_center))
+        return fail(MOE_EINVAL, "%s: eps must be in (0, 1] and the gain centre a number", name);
+    if (T == 0 || H == 0) return MOE_OK;
+    if (residual && !sum) return fail(MOE_EINVAL, "%s: a residual needs the buffer of the sum", name);
+    if ((residual && !aligned16(residual)) || (sum && !aligned16(sum)) || (norm_weight && !aligned16(norm_weight)))
+        return fail(MOE_EINVAL, "%s: pointers must be 16-byte aligned", name);
+    if ((residual && (residual_row_stride < H || residual_row_stride % 8)) ||
+        (sum && (sum_row_stride < H || sum_row_stride % 8)))
+        return fail(MOE_EINVAL, "%s: row strides must be >= H and multiples of 8", name);
+    if (sum && ((sum == residual && sum_row_stride != residual_row_stride) ||
+                (sum == x && sum_row_stride != x_row_stride)))
+        return fail(MOE_EINVAL, "%s: a sum in place of an input needs its row stride", name);
+    AnArgs a{x, x_row_stride, residual, residual_row_stride, norm_weight, gain_center, eps, T, H, sum, sum_row_stride,
+             codes, sf};
+    if (fmt == MOE_MX_E2M1) launch_add_norm<MOE_MX_E2M1>(a, (hipStream_t)stream);
+    else launch_add_norm<MOE_MX_E4M3>(a, (hipStream_t)stream);
+    return check_launch(name);
+}
