@@ -17,6 +17,8 @@
 // not), which costs about 1.5e-5 of a result (3.3e-5 where one value in a
 // hundred is an outlier): far below bf16's rounding, but not fp32's; hence no
 // fp32 output for them.
+#include <type_traits>
+
 #include "experts.hpp"
 #include "mx.hpp"
 
@@ -155,24 +157,39 @@ __global__ void __launch_bounds__(64 * kSkWaves) mx_gemm_skinny_kernel(MgArgs a)
 
 // ------------------------------------------------------------------ many tokens
 // A workgroup of 4 waves (2 x 2) computes a 64 MW x 64 NW block of the output,
-// a wave MW x NW MFMA tiles of 32 x 32, over K in stages of 128 bytes a token
-// row (256 elements in e2m1, 128 in e4m3). Both operands go from global memory
-// to LDS directly (16 bytes a lane, two stage buffers): the copy of stage
-// s + 2 is issued when every wave has read the last of stage s, behind the
-// stage's one barrier, and that barrier stands before the stage's last step's
-// MFMAs, whose operands are in registers by then, so the matrix cores run
-// through it. A step's operands are read from LDS during the step before.
+// a wave MW x NW MFMA tiles of 32 x 32, over K in stages of 128 bytes of a
+// token's row: 256 elements in e2m1, 128 in e4m3 (4 or 2 MFMA steps). Whole
+// cache lines: with 64-byte pieces of e2m1 rows a stage, each line was fetched
+// from the L2 twice, and the L2 bounds the copies (a CU gets about 45 bytes
+// a ns).
+//
+// Codes and scales go from global memory to LDS directly, into a ring of kRing
+// stage buffers. A stage has one barrier, before its last step's MFMAs: every
+// wave's reads of the stage are in registers by then (a step's operands are
+// read during the step before) and the next stage's copies have landed; after
+// it, the copies of stage s + kRing go into the buffer just freed, spread over
+// the MFMAs that follow. So the matrix cores run through the barrier, and the
+// wait before it leaves the younger stages' copies in flight (vmcnt counts them
+// in order, and every wave issues the same number).
 //
 // LDS rows are 128 bytes (64 for e2m1 weights beside e4m3 tokens) without
 // padding, which the direct copies do not allow; the 16-byte chunks of a row
 // are XOR-permuted so that 16 consecutive rows' reads of one chunk spread over
 // all 64 banks.
-template <int FA, int FW>
+template <int FA, int FW, int MW, int NW>
 struct MgShape {
-    static constexpr int kElems = FA == MOE_MX_E2M1 ? 256 : 128;     // K elements a stage
-    static constexpr int kSteps = kElems / 64;
-    static constexpr int kABytes = 128;
-    static constexpr int kWBytes = FW == MOE_MX_E2M1 ? kElems / 2 : kElems;
+    static constexpr int kBM = 64 * MW, kBN = 64 * NW;
+    static constexpr int kElems = FA == MOE_MX_E2M1 ? 256 : 128, kSteps = kElems / 64;    // K of a stage
+    static constexpr int kABytes = 128, kWBytes = FW == MOE_MX_E2M1 ? kElems / 2 : kElems;
+    static constexpr int kSf = kElems / 32;                                               // scale bytes of a row
+    static constexpr int kACopies = kBM * kABytes / 4096, kWCopies = kBN * kWBytes / 4096;   // a wave's, per stage
+    static constexpr int kASfCopies = kBM * kSf / 1024 > 0 ? kBM * kSf / 1024 : 1;
+    static constexpr int kWSfCopies = kBN * kSf / 1024 > 0 ? kBN * kSf / 1024 : 1;
+    static constexpr int kW = kBM * kABytes, kASf = kW + kBN * kWBytes, kWSf = kASf + kSf * kBM;
+    static constexpr int kStage = kWSf + kSf * kBN;
+    // as many stages, 2 to 4, as leave a CU 1 (256 x 256), 2 or 3 workgroups
+    static constexpr int kBudget = 160 * 1024 / (MW * NW >= 16 ? 1 : MW * NW >= 4 ? 2 : 3);
+    static constexpr int kRing = 4 * kStage <= kBudget ? 4 : 3 * kStage <= kBudget ? 3 : 2;
 };
 
 template <int BYTES>
@@ -181,8 +198,13 @@ __device__ __forceinline__ int mg_swizzle(int chunk, int row) {
     else return chunk ^ ((row >> 2) & 3);
 }
 
-// One operand's share of a stage copy by one wave: instruction q of the wave
-// covers 1 KB, the rows [ROWS_PER (4 q + wave), + ROWS_PER).
+// Direct-to-LDS load of 4 bytes a lane, as lds_copy16.
+__device__ __forceinline__ void lds_copy4(u32x4 rsrc, uint32_t lds, uint32_t voff, uint32_t soff) {
+    asm volatile("buffer_load_dword %0, %1, %2 offen lds" :: "v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds) : "memory");
+}
+
+// One operand's codes: instruction q of a wave copies 1 KB, the rows
+// [kRowsPer (4 q + wave), + kRowsPer) of a stage.
 template <int BYTES, int COPIES>
 struct MgCopy {
     static constexpr int kChunks = BYTES / 16, kRowsPer = 64 / kChunks;
@@ -200,25 +222,49 @@ struct MgCopy {
             off[q] = (uint32_t)((r < rows_left ? r : rows_left - 1) * row_bytes + chunk * 16);
         }
     }
-    // stage s into LDS at lds; row_bytes: chunks from there on (the last stage's
-    // tail) are out of the descriptor's range and arrive as zeros
-    __device__ __forceinline__ void issue(uint32_t lds, int s, int wave, int row_bytes) const {
-        const bool in = s * BYTES + chunk * 16 < row_bytes;
-#pragma unroll
-        for (int q = 0; q < COPIES; ++q)
-            lds_copy16(rsrc, __builtin_amdgcn_readfirstlane(lds + (4 * q + wave) * 1024),
-                       in ? off[q] : 0x80000000u, (uint32_t)(s * BYTES));
+    // instruction q of stage s into LDS at lds. Chunks from row_bytes on (the
+    // last stage's tail, stages behind it) are out of the descriptor's range and
+    // arrive as zeros.
+    __device__ __forceinline__ void issue(uint32_t lds, int s, int q, int wave, int row_bytes) const {
+        lds_copy16(rsrc, __builtin_amdgcn_readfirstlane(lds + (4 * q + wave) * 1024),
+                   s * BYTES + chunk * 16 < row_bytes ? off[q] : 0x80000000u, (uint32_t)(s * BYTES));
     }
 };
 
-template <int FMT, int BYTES, int BLOCK_STRIDE>
+// One operand's scales where a row's are whole aligned words (K / 32 a multiple
+// of 4): SF bytes of each of ROWS rows a stage, one word a lane. Blocks of few
+// rows take less than one instruction a wave: waves then repeat each other's,
+// so that all count alike.
+template <int SF, int ROWS, int COPIES>
+struct MgScaleCopy {
+    static constexpr int kWords = SF / 4, kRowsPer = 64 / kWords, kParts = ROWS / kRowsPer;
+    u32x4 rsrc;
+    uint32_t off[COPIES];
+    int word;
+    __device__ __forceinline__ void init(const uint8_t* base, int nb, int rows_left, int wave, int lane) {
+        rsrc = buffer_desc(base);
+        word = 4 * (lane % kWords);
+#pragma unroll
+        for (int q = 0; q < COPIES; ++q) {
+            const int r = kRowsPer * ((4 * q + wave) % kParts) + lane / kWords;
+            off[q] = (uint32_t)((r < rows_left ? r : rows_left - 1) * nb + word);
+        }
+    }
+    __device__ __forceinline__ void issue(uint32_t lds, int s, int q, int wave, int nb) const {
+        lds_copy4(rsrc, __builtin_amdgcn_readfirstlane(lds + (4 * q + wave) % kParts * 256),
+                  s * SF + word < nb ? off[q] : 0x80000000u, (uint32_t)(s * SF));
+    }
+};
+
+// A lane's operand of a step: e2m1, one block (of 4 steps: block 4 g + step, so
+// that a group's scales are one word; of 2: block 2 step + g, e4m3's order);
+// e4m3, its share of blocks 2 step and 2 step + 1.
+template <int FMT, int BYTES, int STEPS>
 __device__ __forceinline__ MxFrag<FMT> mg_read(const uint8_t* rows, int row, int g, int step) {
     MxFrag<FMT> f;
     const uint8_t* p = rows + row * BYTES;
     if constexpr (FMT == MOE_MX_E2M1) {
-        // block of (group, step): 4 g + step where a stage has 4 steps (its four
-        // scales are one word), else 2 step + g, e4m3's order
-        const int c = BLOCK_STRIDE == 4 ? 4 * g + step : 2 * step + g;
+        const int c = STEPS == 4 ? 4 * g + step : 2 * step + g;
         f.q[0] = *reinterpret_cast<const uint4*>(p + 16 * mg_swizzle<BYTES>(c, row));
     } else {
         f.q[0] = *reinterpret_cast<const uint4*>(p + 16 * mg_swizzle<BYTES>(4 * step + g, row));
@@ -227,25 +273,13 @@ __device__ __forceinline__ MxFrag<FMT> mg_read(const uint8_t* rows, int row, int
     return f;
 }
 
-template <int FA, int FW, int MW, int NW, int STEP>
-__device__ __forceinline__ void mg_mfma(mx_f16v (&acc)[MW][NW], const MxFrag<FA> (&fa)[MW], const MxFrag<FW> (&fw)[NW],
-                                        const uint32_t (&sa)[MW], const uint32_t (&sw)[NW]) {
-    constexpr int sel = MgShape<FA, FW>::kSteps == 4 ? STEP : 2 * STEP;
-#pragma unroll
-    for (int m = 0; m < MW; ++m)
-#pragma unroll
-        for (int n = 0; n < NW; ++n)
-            acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[n].reg(), fa[m].reg(), acc[m][n],
-                                                                       mfma_fmt<FW>(), mfma_fmt<FA>(), sel, (int)sw[n],
-                                                                       sel, (int)sa[m]);
-}
-
-template <int FA, int FW, int MW, int NW, bool ALIGNED>
+template <int FA, int FW, int MW, int NW, bool ALIGNED, bool F32>
 __global__ void __launch_bounds__(256, MW * NW >= 16 ? 1 : 2) mx_gemm_tiled_kernel(MgArgs a) {
-    using S = MgShape<FA, FW>;
-    constexpr int BM = 64 * MW, BN = 64 * NW, kStageBytes = BM * S::kABytes + BN * S::kWBytes;
-    constexpr int kOutRow = 32 * NW * 4 + 16;           // one token's columns of a wave in the epilogue, fp32
-    constexpr int kLds = 2 * kStageBytes > 4 * 32 * kOutRow ? 2 * kStageBytes : 4 * 32 * kOutRow;
+    using S = MgShape<FA, FW, MW, NW>;
+    constexpr int kOutRow = 32 * NW * (F32 ? 4 : 2) + 16;       // one token's columns of a wave in the epilogue
+    constexpr int kLds = S::kRing * S::kStage > 4 * 32 * kOutRow ? S::kRing * S::kStage : 4 * 32 * kOutRow;
+    constexpr int kCodeCopies = S::kACopies + S::kWCopies;
+    constexpr int kAll = kCodeCopies + (ALIGNED ? S::kASfCopies + S::kWSfCopies : 0);
     __shared__ __align__(16) uint8_t lds[kLds];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 31, g = lane >> 5, wm = wave >> 1, wn = wave & 1;
@@ -254,55 +288,75 @@ __global__ void __launch_bounds__(256, MW * NW >= 16 ? 1 : 2) mx_gemm_tiled_kern
     // round robin) gets a contiguous run of them, and a run goes through groups
     // of 8 rows of blocks column by column, so that an XCD's L2 holds what its
     // workgroups share.
-    const int mt = (a.T + BM - 1) / BM, nt = (a.N + BN - 1) / BN, tiles = mt * nt;
+    const int mt = (a.T + S::kBM - 1) / S::kBM, nt = (a.N + S::kBN - 1) / S::kBN, tiles = mt * nt;
     const int x = blockIdx.x & 7, per = tiles >> 3, more = tiles & 7;
     const int id = x * per + (x < more ? x : more) + (int)(blockIdx.x >> 3);
     const int group = id / (8 * nt), gm0 = group * 8, gh = mt - gm0 < 8 ? mt - gm0 : 8, in = id - gm0 * nt;
-    const int64_t m0 = (int64_t)(gm0 + in % gh) * BM, n0 = (int64_t)(in / gh) * BN;
+    const int64_t m0 = (int64_t)(gm0 + in % gh) * S::kBM, n0 = (int64_t)(in / gh) * S::kBN;
 
     const int nb = a.K >> 5, a_row = (int)mx_bytes(a.K, FA), w_row = (int)mx_bytes(a.K, FW);
     const int stages = (a.K + S::kElems - 1) / S::kElems;
-    MgCopy<S::kABytes, BM * S::kABytes / 4096> ca;
-    MgCopy<S::kWBytes, BN * S::kWBytes / 4096> cw;
-    ca.init(a.a + m0 * a_row, a_row, (int)(a.T - m0 < BM ? a.T - m0 : BM), wave, lane);
-    cw.init(a.w + n0 * w_row, w_row, (int)(a.N - n0 < BN ? a.N - n0 : BN), wave, lane);
+    const int rows_m = (int)(a.T - m0 < S::kBM ? a.T - m0 : S::kBM), rows_n = (int)(a.N - n0 < S::kBN ? a.N - n0 : S::kBN);
+    MgCopy<S::kABytes, S::kACopies> ca;
+    MgCopy<S::kWBytes, S::kWCopies> cw;
+    MgScaleCopy<S::kSf, S::kBM, S::kASfCopies> csa;
+    MgScaleCopy<S::kSf, S::kBN, S::kWSfCopies> csw;
+    ca.init(a.a + m0 * a_row, a_row, rows_m, wave, lane);
+    cw.init(a.w + n0 * w_row, w_row, rows_n, wave, lane);
+    if constexpr (ALIGNED) {
+        csa.init(a.a_sf + m0 * nb, nb, rows_m, wave, lane);
+        csw.init(a.w_sf + n0 * nb, nb, rows_n, wave, lane);
+    }
     const uint32_t lds0 = lds_addr(lds);
-    auto copy = [&](int s) {
-        const uint32_t at = lds0 + (s & 1) * kStageBytes;
-        ca.issue(at, s, wave, a_row);
-        cw.issue(at + BM * S::kABytes, s, wave, w_row);
+    auto copy = [&](int s, int q0, int q1) {        // instructions [q0, q1) of stage s's kAll
+        const uint32_t at = lds0 + (s % S::kRing) * S::kStage;
+#pragma unroll
+        for (int q = q0; q < q1; ++q) {
+            if (q < S::kACopies) ca.issue(at, s, q, wave, a_row);
+            else if (q < kCodeCopies) cw.issue(at + S::kW, s, q - S::kACopies, wave, w_row);
+            else if (q < kCodeCopies + S::kASfCopies) csa.issue(at + S::kASf, s, q - kCodeCopies, wave, nb);
+            else csw.issue(at + S::kWSf, s, q - kCodeCopies - S::kASfCopies, wave, nb);
+        }
     };
+    // scales from global memory (K / 32 not a multiple of 4): row pointers
     const uint8_t *pa_sf[MW], *pw_sf[NW];
+    if constexpr (!ALIGNED) {
 #pragma unroll
-    for (int m = 0; m < MW; ++m) {
-        const int64_t t = m0 + 32 * (wm * MW + m) + r;
-        pa_sf[m] = a.a_sf + (t < a.T ? t : a.T - 1) * nb;
+        for (int m = 0; m < MW; ++m) {
+            const int t = 32 * (wm * MW + m) + r;
+            pa_sf[m] = a.a_sf + (m0 + (t < rows_m ? t : rows_m - 1)) * nb;
+        }
+#pragma unroll
+        for (int n = 0; n < NW; ++n) {
+            const int c = 32 * (wn * NW + n) + r;
+            pw_sf[n] = a.w_sf + (n0 + (c < rows_n ? c : rows_n - 1)) * nb;
+        }
     }
-#pragma unroll
-    for (int n = 0; n < NW; ++n) {
-        const int64_t c = n0 + 32 * (wn * NW + n) + r;
-        pw_sf[n] = a.w_sf + (c < a.N ? c : a.N - 1) * nb;
-    }
-    // a stage's scales of the lane's rows: the word of group g's 4 blocks, or
-    // (2 steps) the stage's word moved so that step s's byte is 2 s
-    auto scales = [&](int s, uint32_t (&sa)[MW], uint32_t (&sw)[NW]) {
-        const int b0 = s * (S::kElems / 32) + (S::kSteps == 4 ? 4 * g : 0), shift = S::kSteps == 4 ? 0 : 8 * g;
-#pragma unroll
-        for (int m = 0; m < MW; ++m) sa[m] = scale_word<ALIGNED>(pa_sf[m], b0, nb) >> shift;
-#pragma unroll
-        for (int n = 0; n < NW; ++n) sw[n] = scale_word<ALIGNED>(pw_sf[n], b0, nb) >> shift;
+    // a stage's scales of one of the lane's rows: the word of group g's 4 blocks,
+    // step s's in byte s; of 2 steps, the stage's word moved so that it is byte 2 s
+    auto scale = [&](int s, const uint8_t* at, const uint8_t* row_sf, int row) {
+        const int w = S::kSteps == 4 ? 4 * g : 0;
+        const uint32_t v = ALIGNED ? *reinterpret_cast<const uint32_t*>(at + S::kSf * row + w)
+                                   : scale_word<false>(row_sf, S::kSf * s + w, nb);
+        return S::kSteps == 4 ? v : v >> (8 * g);
     };
-    MxFrag<FA> fa[2][MW];
-    MxFrag<FW> fw[2][NW];
-    auto read = [&](int s, int step, int f) {
-        const uint8_t* pa = lds + (s & 1) * kStageBytes;
-        const uint8_t* pw = pa + BM * S::kABytes;
+    auto scales = [&](int s, uint32_t (&sa)[MW], uint32_t (&sw)[NW]) {
+        const uint8_t* at = lds + (s % S::kRing) * S::kStage;
 #pragma unroll
-        for (int m = 0; m < MW; ++m)
-            fa[f][m] = mg_read<FA, S::kABytes, S::kSteps>(pa, 32 * (wm * MW + m) + r, g, step);
+        for (int m = 0; m < MW; ++m) sa[m] = scale(s, at + S::kASf, pa_sf[m], 32 * (wm * MW + m) + r);
 #pragma unroll
-        for (int n = 0; n < NW; ++n)
-            fw[f][n] = mg_read<FW, S::kWBytes, S::kSteps>(pw, 32 * (wn * NW + n) + r, g, step);
+        for (int n = 0; n < NW; ++n) sw[n] = scale(s, at + S::kWSf, pw_sf[n], 32 * (wn * NW + n) + r);
+    };
+    struct Operands {
+        MxFrag<FA> a[MW];
+        MxFrag<FW> w[NW];
+    };
+    auto read = [&](int s, int step, Operands& o) {
+        const uint8_t* at = lds + (s % S::kRing) * S::kStage;
+#pragma unroll
+        for (int n = 0; n < NW; ++n) o.w[n] = mg_read<FW, S::kWBytes, S::kSteps>(at + S::kW, 32 * (wn * NW + n) + r, g, step);
+#pragma unroll
+        for (int m = 0; m < MW; ++m) o.a[m] = mg_read<FA, S::kABytes, S::kSteps>(at, 32 * (wm * MW + m) + r, g, step);
     };
 
     mx_f16v acc[MW][NW];
@@ -312,44 +366,64 @@ __global__ void __launch_bounds__(256, MW * NW >= 16 ? 1 : 2) mx_gemm_tiled_kern
         for (int n = 0; n < NW; ++n)
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[m][n][i] = 0.0f;
+    uint32_t sa[MW], sw[NW], sa1[MW], sw1[NW];
+    // one MFMA row of a step; the scales' byte SEL
+    auto mfma = [&](const Operands& o, int m, auto sel) {
+#pragma unroll
+        for (int n = 0; n < NW; ++n)
+            acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(o.w[n].reg(), o.a[m].reg(), acc[m][n],
+                                                                        mfma_fmt<FW>(), mfma_fmt<FA>(), sel.value,
+                                                                        (int)sw[n], sel.value, (int)sa[m]);
+    };
+    auto mfmas = [&](const Operands& o, auto sel) {
+#pragma unroll
+        for (int m = 0; m < MW; ++m) mfma(o, m, sel);
+        __builtin_amdgcn_sched_barrier(0);
+    };
 
-    uint32_t sa[2][MW], sw[2][NW];
-    copy(0);
-    scales(0, sa[0], sw[0]);
-    if (stages > 1) copy(1);
-    __builtin_amdgcn_s_waitcnt(vmcnt_at_most(0));
+#pragma unroll
+    for (int s = 0; s < S::kRing; ++s) copy(s, 0, kAll);
+    Operands o0, o1;
+    if constexpr (!ALIGNED) scales(0, sa, sw);
+    __builtin_amdgcn_s_waitcnt(vmcnt_at_most((S::kRing - 1) * kAll));
     __syncthreads();
-    read(0, 0, 0);
+    if constexpr (ALIGNED) scales(0, sa, sw);
+    read(0, 0, o0);
     for (int s = 0; s < stages; ++s) {
-        if (s + 1 < stages) scales(s + 1, sa[1], sw[1]);
+        read(s, 1, o1);
+        if constexpr (!ALIGNED) scales(s + 1, sa1, sw1);
+        mfmas(o0, std::integral_constant<int, 0>());
         if constexpr (S::kSteps == 4) {
-            read(s, 1, 1);
-            mg_mfma<FA, FW, MW, NW, 0>(acc, fa[0], fw[0], sa[0], sw[0]);
-            read(s, 2, 0);
-            mg_mfma<FA, FW, MW, NW, 1>(acc, fa[1], fw[1], sa[0], sw[0]);
-            read(s, 3, 1);
-            mg_mfma<FA, FW, MW, NW, 2>(acc, fa[0], fw[0], sa[0], sw[0]);
-        } else {
-            read(s, 1, 1);
-            mg_mfma<FA, FW, MW, NW, 0>(acc, fa[0], fw[0], sa[0], sw[0]);
+            read(s, 2, o0);
+            mfmas(o1, std::integral_constant<int, 1>());
+            read(s, 3, o1);
+            mfmas(o0, std::integral_constant<int, 2>());
         }
-        // every wave's operands of the stage's last step are in registers, and
-        // the next stage's copies have landed
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (s + 2 < stages) copy(s + 2);
-        if (s + 1 < stages) read(s + 1, 0, 0);
-        mg_mfma<FA, FW, MW, NW, S::kSteps - 1>(acc, fa[1], fw[1], sa[0], sw[0]);
+        __builtin_amdgcn_s_waitcnt(vmcnt_at_most((S::kRing - 2) * kAll) & lgkmcnt_zero());
+        asm volatile("s_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (ALIGNED) scales(s + 1, sa1, sw1);
+        read(s + 1, 0, o0);
 #pragma unroll
-        for (int m = 0; m < MW; ++m) sa[0][m] = sa[1][m];
+        for (int m = 0; m < MW; ++m) {
+            copy(s + S::kRing, m * kAll / MW, (m + 1) * kAll / MW);
+            mfma(o1, m, std::integral_constant<int, S::kSteps == 4 ? 3 : 2>());
+            __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll
-        for (int n = 0; n < NW; ++n) sw[0][n] = sw[1][n];
+        for (int m = 0; m < MW; ++m) sa[m] = sa1[m];
+#pragma unroll
+        for (int n = 0; n < NW; ++n) sw[n] = sw1[n];
     }
+    // the copies of the stages behind the last still write (zeros) to the LDS
+    __builtin_amdgcn_s_waitcnt(vmcnt_at_most(0) & lgkmcnt_zero());
+    __syncthreads();
 
     // Epilogue: a lane holds 4 consecutive columns of one token at a time. Each
-    // wave turns 32 tokens of its columns through its own part of the LDS (free
-    // since the last barrier) and stores whole 16-byte pieces of a token's row.
+    // wave turns 32 tokens of its columns through its own part of the LDS and
+    // stores whole 16-byte pieces of a token's row.
+    constexpr int kEs = F32 ? 4 : 2, kPiece = 16 / kEs, kPieces = 32 * NW / kPiece;
     uint8_t* slab = lds + wave * 32 * kOutRow;
-    const int es = a.out_f32 ? 4 : 2, piece = 16 / es, pieces = 32 * NW / piece;
 #pragma unroll
     for (int m = 0; m < MW; ++m) {
         wave_lds_sync();
@@ -359,31 +433,44 @@ __global__ void __launch_bounds__(256, MW * NW >= 16 ? 1 : 2) mx_gemm_tiled_kern
             for (int q = 0; q < 4; ++q) {
                 const int c = 32 * n + 8 * q + 4 * g;
                 const mx_f16v& v = acc[m][n];
-                if (a.out_f32)
+                if constexpr (F32)
                     *reinterpret_cast<floatx4*>(slab + r * kOutRow + c * 4) =
                         floatx4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
                 else
                     *reinterpret_cast<uint2*>(slab + r * kOutRow + c * 2) =
-                        make_uint2(f32_to_bf16(v[4 * q]) | (f32_to_bf16(v[4 * q + 1]) << 16),
-                                   f32_to_bf16(v[4 * q + 2]) | (f32_to_bf16(v[4 * q + 3]) << 16));
+                        make_uint2(bf16x2_pack(v[4 * q], v[4 * q + 1]), bf16x2_pack(v[4 * q + 2], v[4 * q + 3]));
             }
         wave_lds_sync();
-        for (int i = lane; i < 32 * pieces; i += 64) {
-            const int tr = i / pieces, c = (i - tr * pieces) * piece;
+#pragma unroll
+        for (int j = 0; j < 32 * kPieces / 64; ++j) {
+            const int i = lane + 64 * j, tr = i / kPieces, c = (i % kPieces) * kPiece;
             const int64_t t = m0 + 32 * (wm * MW + m) + tr, n = n0 + 32 * NW * wn + c;
             if (t >= a.T || n >= a.N) continue;
-            const uint8_t* src = slab + tr * kOutRow + c * es;
-            uint8_t* dst = (uint8_t*)a.out + (t * a.out_stride + n) * es;
-            if (a.out_vec && n + piece <= a.N) {
+            const uint8_t* src = slab + tr * kOutRow + c * kEs;
+            uint8_t* dst = (uint8_t*)a.out + (t * a.out_stride + n) * kEs;
+            if (a.out_vec && n + kPiece <= a.N) {
                 *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
             } else {
-                for (int j = 0; j < piece && n + j < a.N; ++j) {
-                    if (a.out_f32) reinterpret_cast<float*>(dst)[j] = reinterpret_cast<const float*>(src)[j];
-                    else reinterpret_cast<uint16_t*>(dst)[j] = reinterpret_cast<const uint16_t*>(src)[j];
+                for (int e = 0; e < kPiece && n + e < a.N; ++e) {
+                    if constexpr (F32) reinterpret_cast<float*>(dst)[e] = reinterpret_cast<const float*>(src)[e];
+                    else reinterpret_cast<uint16_t*>(dst)[e] = reinterpret_cast<const uint16_t*>(src)[e];
                 }
             }
         }
     }
+}
+
+template <int FA, int FW, int MW, int NW, bool ALIGNED>
+void launch_mx_tiled(const MgArgs& a, hipStream_t s) {
+    const int64_t tiles = (int64_t)((a.T + 64 * MW - 1) / (64 * MW)) * ((a.N + 64 * NW - 1) / (64 * NW));
+    const dim3 g((unsigned)tiles), b(256);
+    if constexpr (FA == MOE_MX_E2M1) {
+        if (a.out_f32) {
+            hipLaunchKernelGGL((mx_gemm_tiled_kernel<FA, FW, MW, NW, ALIGNED, true>), g, b, 0, s, a);
+            return;
+        }
+    }
+    hipLaunchKernelGGL((mx_gemm_tiled_kernel<FA, FW, MW, NW, ALIGNED, false>), g, b, 0, s, a);
 }
 
 template <int FA, int FW, bool ALIGNED>
@@ -399,12 +486,9 @@ int launch_mx_gemm(const MgArgs& a, hipStream_t s) {
     const auto tiles = [&](int bm, int bn) { return (int64_t)((a.T + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
     if (tiles(64, 64) > 0x7FFFFFFF) return fail(MOE_EUNSUPPORTED, "%s: too many output tiles", name);
     // the largest tile that still gives every CU one
-    if (tiles(256, 256) >= 192)
-        hipLaunchKernelGGL((mx_gemm_tiled_kernel<FA, FW, 4, 4, ALIGNED>), dim3((unsigned)tiles(256, 256)), dim3(256), 0, s, a);
-    else if (tiles(128, 128) >= 192)
-        hipLaunchKernelGGL((mx_gemm_tiled_kernel<FA, FW, 2, 2, ALIGNED>), dim3((unsigned)tiles(128, 128)), dim3(256), 0, s, a);
-    else
-        hipLaunchKernelGGL((mx_gemm_tiled_kernel<FA, FW, 1, 1, ALIGNED>), dim3((unsigned)tiles(64, 64)), dim3(256), 0, s, a);
+    if (tiles(256, 256) >= 192) launch_mx_tiled<FA, FW, 4, 4, ALIGNED>(a, s);
+    else if (tiles(128, 128) >= 192) launch_mx_tiled<FA, FW, 2, 2, ALIGNED>(a, s);
+    else launch_mx_tiled<FA, FW, 1, 1, ALIGNED>(a, s);
     return check_launch(name);
 }
 

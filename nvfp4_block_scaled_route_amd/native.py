@@ -129,8 +129,8 @@ def _ptr(t) -> int | None:
 
 
 def _stream(stream) -> int | None:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:   # the current stream of the current device, without the objects around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -309,108 +309,146 @@ def moe_finalize(rows, n_partials, partial_stride, exp2perm, topk_weights, norm_
 
 # ------------------------------------------------------------------ MX formats, tokens by expert
 # These calls check shapes, types, layouts and devices of their tensors here:
-# the library sees addresses only.
-_BF16_TYPES = (torch.bfloat16, torch.int16)     # int16, uint16: bf16 bit patterns
-if hasattr(torch, "uint16"):
-    _BF16_TYPES += (torch.uint16,)
+# the library sees addresses only. A decode step's calls are as long as their
+# checks, so a tensor that is in order passes one short test (_rows, _flat);
+# one that is not goes to _refuse, which finds the reason.
+_BF16_TYPES = (torch.bfloat16, torch.int16, torch.uint16)     # int16, uint16: bf16 bit patterns
+_TYPED_ROWS = _BF16_TYPES + (torch.float32,)
+_U8, _I32, _F32 = (torch.uint8,), (torch.int32,), (torch.float32,)
+_E4M3_TYPES = (torch.uint8, torch.float8_e4m3fn)
+_SF_TYPES = (torch.uint8, torch.float8_e8m0fnu)
 
 
-def _arg(call, name, t, dtypes, shape, strided=False, stream=None) -> int:
-    """Checks one tensor argument and returns its row stride in elements: of one
-    of `dtypes`, of `shape`, on the current device (and the stream's), rows of
-    consecutive elements, and these contiguous unless `strided`."""
+def _refuse(call, name, t, dtypes, shape, dev):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{call}: {name} must be a torch tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{call}: {name} has type {t.dtype}, not {' or '.join(str(d) for d in dtypes)}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{call}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     if not t.is_cuda:
         raise ValueError(f"{call}: {name} must be a device tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{call}: {name} is on {t.device}, not on the current device")
-    if stream is not None and hasattr(stream, "device") and stream.device != t.device:
-        raise ValueError(f"{call}: {name} is on {t.device}, the stream on {stream.device}")
-    if strided and t.dim() == 2:
-        if t.shape[1] > 1 and t.stride(1) != 1:
-            raise ValueError(f"{call}: the rows of {name} must be contiguous")
-        return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 16) * 16   # one row: any stride will do
-    if not t.is_contiguous():
+    if t.get_device() != dev:
+        raise ValueError(f"{call}: {name} is on {t.device}, not on the current device (or the stream's)")
+    raise ValueError(f"{call}: {name} must have contiguous rows{'' if len(shape) == 2 else ' of no stride'}")
+
+
+def _rows(call, name, t, dtypes, shape, dev) -> int:
+    """The row stride in elements of a matrix of one of `dtypes`, of `shape`, on
+    device `dev`, with rows of consecutive elements."""
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.get_device() == dev:
+        if shape[0] <= 1:
+            if shape[1] <= 1 or t.stride(1) == 1:
+                return (shape[1] + 15) // 16 * 16       # one row: any stride will do
+        else:
+            s = t.stride()
+            if s[1] == 1 or shape[1] <= 1:
+                return s[0]
+    return _refuse(call, name, t, dtypes, shape, dev)
+
+
+def _flat(call, name, t, dtypes, shape, dev) -> int:
+    """The address of a contiguous tensor of one of `dtypes`, of `shape`, on device `dev`."""
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        return t.data_ptr()
+    if isinstance(t, torch.Tensor) and not t.is_contiguous() and t.shape == shape:
         raise ValueError(f"{call}: {name} must be contiguous")
-    return t.shape[-1] if t.dim() else 1
+    return _refuse(call, name, t, dtypes, shape, dev)
 
 
-def _shape2(call, name, t) -> tuple[int, int]:
+def _where(call, t, stream) -> tuple[int, int]:
+    """The device that every tensor has to be on, the current one, and the raw
+    stream; a stream object must be of that device. -2 stands for no device: the
+    first tensor is a host tensor, which the checks refuse."""
+    if t.get_device() < 0:
+        return -2, 0
+    dev = torch.cuda.current_device()
+    if stream is None:
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    if hasattr(stream, "cuda_stream"):
+        if stream.device.index != dev:
+            raise ValueError(f"{call}: the stream is on {stream.device}, not on the current device")
+        return dev, stream.cuda_stream
+    return dev, int(stream)
+
+
+def _shape2(call, name, t):
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{call}: {name} must be a tensor of two dimensions")
-    return t.shape[0], t.shape[1]
+    return t.shape
 
 
-def _mx_args(call, T, H, fmt, codes, sf, stream) -> None:
-    if fmt not in (MOE_MX_E2M1, MOE_MX_E4M3):
-        raise ValueError(f"{call}: format {fmt!r} is neither MOE_MX_E2M1 nor MOE_MX_E4M3")
+def _mx(call, T, H, fmt, codes, sf, dev) -> tuple[int, int]:
+    """The addresses of [T, H] values' codes and scales."""
     if H % 32:
         raise MoeError(f"{call}: {H} elements a row are not a multiple of 32")
-    types = (torch.uint8,) if fmt == MOE_MX_E2M1 else (torch.uint8, torch.float8_e4m3fn)
-    _arg(call, "codes", codes, types, (T, H // 2 if fmt == MOE_MX_E2M1 else H), stream=stream)
-    _arg(call, "sf", sf, (torch.uint8, torch.float8_e8m0fnu), (T, H // 32), stream=stream)
+    if fmt == MOE_MX_E2M1:
+        c = _flat(call, "codes", codes, _U8, (T, H // 2), dev)
+    elif fmt == MOE_MX_E4M3:
+        c = _flat(call, "codes", codes, _E4M3_TYPES, (T, H), dev)
+    else:
+        raise ValueError(f"{call}: format {fmt!r} is neither MOE_MX_E2M1 nor MOE_MX_E4M3")
+    return c, _flat(call, "sf", sf, _SF_TYPES, (T, H // 32), dev)
 
 
 def mx_quant(x, fmt, codes, sf, stream=None) -> None:
     """bf16 x [T, H] -> MX codes [T, H/2] or [T, H] and e8m0 scales [T, H/32]."""
-    T, H = _shape2("mx_quant", "x", x)
-    ld = _arg("mx_quant", "x", x, _BF16_TYPES, (T, H), True, stream)
-    _mx_args("mx_quant", T, H, fmt, codes, sf, stream)
-    _check(lib().mx_quant(_ptr(x), ld, T, H, fmt, _ptr(codes), _ptr(sf), _stream(stream)), "mx_quant")
+    shape = T, H = _shape2("mx_quant", "x", x)
+    dev, st = _where("mx_quant", x, stream)
+    ld = _rows("mx_quant", "x", x, _BF16_TYPES, shape, dev)
+    c, s = _mx("mx_quant", T, H, fmt, codes, sf, dev)
+    rc = lib().mx_quant(x.data_ptr(), ld, T, H, fmt, c, s, st)
+    if rc:
+        _check(rc, "mx_quant")
 
 
 def mx_dequant(codes, sf, fmt, out, stream=None) -> None:
     """MX codes and scales -> bf16 out [T, H]."""
-    T, H = _shape2("mx_dequant", "out", out)
-    ld = _arg("mx_dequant", "out", out, _BF16_TYPES, (T, H), True, stream)
-    _mx_args("mx_dequant", T, H, fmt, codes, sf, stream)
-    _check(lib().mx_dequant(_ptr(codes), _ptr(sf), T, H, fmt, _ptr(out), ld, _stream(stream)), "mx_dequant")
+    shape = T, H = _shape2("mx_dequant", "out", out)
+    dev, st = _where("mx_dequant", out, stream)
+    ld = _rows("mx_dequant", "out", out, _BF16_TYPES, shape, dev)
+    c, s = _mx("mx_dequant", T, H, fmt, codes, sf, dev)
+    rc = lib().mx_dequant(c, s, T, H, fmt, out.data_ptr(), ld, st)
+    if rc:
+        _check(rc, "mx_dequant")
 
 
 def mx_add_norm_quant(x, residual, norm_weight, gain_center, eps, fmt, sum_out, codes, sf, stream=None) -> None:
     """sum_out = bf16(x + residual), and the MX codes and scales of its RMSNorm.
     residual may be None (sum_out then too); sum_out may be residual or x itself."""
     call = "mx_add_norm_quant"
-    T, H = _shape2(call, "x", x)
-    ld = _arg(call, "x", x, _BF16_TYPES, (T, H), True, stream)
+    shape = T, H = _shape2(call, "x", x)
+    dev, st = _where(call, x, stream)
+    ld = _rows(call, "x", x, _BF16_TYPES, shape, dev)
     ld_res = ld_sum = 0
+    res = out = w = None
     if residual is not None:
-        ld_res = _arg(call, "residual", residual, _BF16_TYPES, (T, H), True, stream)
+        ld_res, res = _rows(call, "residual", residual, _BF16_TYPES, shape, dev), residual.data_ptr()
     if sum_out is not None:
-        ld_sum = _arg(call, "sum_out", sum_out, _BF16_TYPES, (T, H), True, stream)
+        ld_sum, out = _rows(call, "sum_out", sum_out, _BF16_TYPES, shape, dev), sum_out.data_ptr()
     if norm_weight is not None:
-        _arg(call, "norm_weight", norm_weight, _BF16_TYPES, (H,), stream=stream)
-    _mx_args(call, T, H, fmt, codes, sf, stream)
-    _check(lib().mx_add_norm_quant(_ptr(x), ld, _ptr(residual), ld_res, _ptr(norm_weight), float(gain_center),
-                                   float(eps), T, H, fmt, _ptr(sum_out), ld_sum, _ptr(codes), _ptr(sf),
-                                   _stream(stream)), call)
+        w = _flat(call, "norm_weight", norm_weight, _BF16_TYPES, (H,), dev)
+    c, s = _mx(call, T, H, fmt, codes, sf, dev)
+    rc = lib().mx_add_norm_quant(x.data_ptr(), ld, res, ld_res, w, gain_center, eps, T, H, fmt, out, ld_sum, c, s, st)
+    if rc:
+        _check(rc, call)
 
 
 def mx_gemm(a_codes, a_sf, a_fmt, w_codes, w_sf, w_fmt, out, stream=None) -> None:
     """out [T, N] = a [T, K] times w [N, K] transposed, both MX; out bf16, or fp32
     where both are e2m1."""
     call = "mx_gemm"
-    T, N = _shape2(call, "out", out)
+    shape = T, N = _shape2(call, "out", out)
     K = _shape2(call, "a_sf", a_sf)[1] * 32
-    ld = _arg(call, "out", out, _BF16_TYPES + (torch.float32,), (T, N), True, stream)
-    _mx_args(call, T, K, a_fmt, a_codes, a_sf, stream)
-    _mx_args(call, N, K, w_fmt, w_codes, w_sf, stream)
-    _check(lib().mx_gemm(_ptr(a_codes), _ptr(a_sf), a_fmt, _ptr(w_codes), _ptr(w_sf), w_fmt, T, N, K, _ptr(out),
-                         max(ld, N), MOE_F32 if out.dtype == torch.float32 else MOE_BF16, _stream(stream)), call)
-
-
-def _sort_maps(call, exp2perm, perm2tok, total_rows, rows_max, stream) -> tuple[int, int]:
-    T, K = _shape2(call, "exp2perm", exp2perm)
-    _arg(call, "exp2perm", exp2perm, (torch.int32,), (T, K), stream=stream)
-    if perm2tok is not None:
-        _arg(call, "perm2tok", perm2tok, (torch.int32,), (rows_max,), stream=stream)
-        _arg(call, "total_rows", total_rows, (torch.int32,), (1,), stream=stream)
-    return T, K
+    dev, st = _where(call, out, stream)
+    ld = _rows(call, "out", out, _TYPED_ROWS, shape, dev)
+    a, asf = _mx(call, T, K, a_fmt, a_codes, a_sf, dev)
+    w, wsf = _mx(call, N, K, w_fmt, w_codes, w_sf, dev)
+    rc = lib().mx_gemm(a, asf, a_fmt, w, wsf, w_fmt, T, N, K, out.data_ptr(), ld,
+                       MOE_F32 if out.dtype == torch.float32 else MOE_BF16, st)
+    if rc:
+        _check(rc, call)
 
 
 def _row_type(call, rows) -> int:
@@ -423,54 +461,69 @@ def _row_type(call, rows) -> int:
 
 def moe_dispatch(x, exp2perm, perm2tok, total_rows, rows, stream=None) -> None:
     """rows[exp2perm[t, k]] = x[t]; padding rows below total_rows become zeros.
-    x [T, W] and rows [rows_max, W] of one type, any of 1, 2 or 4 bytes."""
+    x [T, W] and rows [rows_max, W] of one type."""
     call = "moe_dispatch"
-    R, W = _shape2(call, "rows", rows)
-    T, K = _sort_maps(call, exp2perm, perm2tok, total_rows, R, stream)
-    ld_x = _arg(call, "x", x, (rows.dtype,), (T, W), True, stream)
-    ld_r = _arg(call, "rows", rows, (rows.dtype,), (R, W), True, stream)
-    es = rows.element_size()
-    _check(lib().moe_dispatch(_ptr(x), ld_x * es, W * es, _ptr(exp2perm), _ptr(perm2tok), _ptr(total_rows), T, K, R,
-                              _ptr(rows), ld_r * es, _stream(stream)), call)
+    shape = R, W = _shape2(call, "rows", rows)
+    maps = T, K = _shape2(call, "exp2perm", exp2perm)
+    dev, st = _where(call, rows, stream)
+    types, es = (rows.dtype,), rows.element_size()
+    ld_x = _rows(call, "x", x, types, (T, W), dev)
+    ld_r = _rows(call, "rows", rows, types, shape, dev)
+    rc = lib().moe_dispatch(x.data_ptr(), ld_x * es, W * es, _flat(call, "exp2perm", exp2perm, _I32, maps, dev),
+                            _flat(call, "perm2tok", perm2tok, _I32, (R,), dev),
+                            _flat(call, "total_rows", total_rows, _I32, (1,), dev), T, K, R, rows.data_ptr(),
+                            ld_r * es, st)
+    if rc:
+        _check(rc, call)
 
 
 def moe_dispatch_bwd(d_rows, exp2perm, d_x, stream=None) -> None:
     """d_x[t] = sum_k d_rows[exp2perm[t, k]]; bf16 or fp32."""
     call = "moe_dispatch_bwd"
-    R, H = _shape2(call, "d_rows", d_rows)
-    dtype = _row_type(call, d_rows)
-    T, K = _sort_maps(call, exp2perm, None, None, R, stream)
-    ld_r = _arg(call, "d_rows", d_rows, (d_rows.dtype,), (R, H), True, stream)
-    ld_x = _arg(call, "d_x", d_x, (d_rows.dtype,), (T, H), True, stream)
-    _check(lib().moe_dispatch_bwd(_ptr(d_rows), ld_r, dtype, _ptr(exp2perm), T, K, R, H, _ptr(d_x), ld_x,
-                                  _stream(stream)), call)
+    shape = R, H = _shape2(call, "d_rows", d_rows)
+    maps = T, K = _shape2(call, "exp2perm", exp2perm)
+    dtype, types = _row_type(call, d_rows), (d_rows.dtype,)
+    dev, st = _where(call, d_rows, stream)
+    ld_r = _rows(call, "d_rows", d_rows, types, shape, dev)
+    ld_x = _rows(call, "d_x", d_x, types, (T, H), dev)
+    rc = lib().moe_dispatch_bwd(d_rows.data_ptr(), ld_r, dtype, _flat(call, "exp2perm", exp2perm, _I32, maps, dev), T,
+                                K, R, H, d_x.data_ptr(), ld_x, st)
+    if rc:
+        _check(rc, call)
 
 
 def moe_combine(rows, exp2perm, topk_weights, out, stream=None) -> None:
     """out[t] = sum_k topk_weights[t, k] * rows[exp2perm[t, k]]; bf16 or fp32 rows."""
     call = "moe_combine"
-    R, H = _shape2(call, "rows", rows)
-    dtype = _row_type(call, rows)
-    T, K = _sort_maps(call, exp2perm, None, None, R, stream)
-    ld_r = _arg(call, "rows", rows, (rows.dtype,), (R, H), True, stream)
-    _arg(call, "topk_weights", topk_weights, (torch.float32,), (T, K), stream=stream)
-    ld_o = _arg(call, "out", out, (rows.dtype,), (T, H), True, stream)
-    _check(lib().moe_combine(_ptr(rows), ld_r, dtype, _ptr(exp2perm), _ptr(topk_weights), T, K, R, H, _ptr(out), ld_o,
-                             _stream(stream)), call)
+    shape = R, H = _shape2(call, "rows", rows)
+    maps = T, K = _shape2(call, "exp2perm", exp2perm)
+    dtype, types = _row_type(call, rows), (rows.dtype,)
+    dev, st = _where(call, rows, stream)
+    ld_r = _rows(call, "rows", rows, types, shape, dev)
+    ld_o = _rows(call, "out", out, types, (T, H), dev)
+    rc = lib().moe_combine(rows.data_ptr(), ld_r, dtype, _flat(call, "exp2perm", exp2perm, _I32, maps, dev),
+                           _flat(call, "topk_weights", topk_weights, _F32, maps, dev), T, K, R, H, out.data_ptr(),
+                           ld_o, st)
+    if rc:
+        _check(rc, call)
 
 
 def moe_combine_bwd(d_out, rows, exp2perm, perm2tok, total_rows, topk_weights, d_rows, d_weights, stream=None) -> None:
     """moe_combine's gradients: d_rows[exp2perm[t, k]] = topk_weights[t, k] * d_out[t] (padding rows
     below total_rows zero) and d_weights[t, k] = <rows[exp2perm[t, k]], d_out[t]>. d_rows may be rows."""
     call = "moe_combine_bwd"
-    R, H = _shape2(call, "rows", rows)
-    dtype = _row_type(call, rows)
-    T, K = _sort_maps(call, exp2perm, perm2tok, total_rows, R, stream)
-    ld_o = _arg(call, "d_out", d_out, (rows.dtype,), (T, H), True, stream)
-    ld_r = _arg(call, "rows", rows, (rows.dtype,), (R, H), True, stream)
-    _arg(call, "topk_weights", topk_weights, (torch.float32,), (T, K), stream=stream)
-    ld_d = _arg(call, "d_rows", d_rows, (rows.dtype,), (R, H), True, stream)
-    _arg(call, "d_weights", d_weights, (torch.float32,), (T, K), stream=stream)
-    _check(lib().moe_combine_bwd(_ptr(d_out), ld_o, _ptr(rows), ld_r, dtype, _ptr(exp2perm), _ptr(perm2tok),
-                                 _ptr(total_rows), _ptr(topk_weights), T, K, R, H, _ptr(d_rows), ld_d, _ptr(d_weights),
-                                 _stream(stream)), call)
+    shape = R, H = _shape2(call, "rows", rows)
+    maps = T, K = _shape2(call, "exp2perm", exp2perm)
+    dtype, types = _row_type(call, rows), (rows.dtype,)
+    dev, st = _where(call, rows, stream)
+    ld_o = _rows(call, "d_out", d_out, types, (T, H), dev)
+    ld_r = _rows(call, "rows", rows, types, shape, dev)
+    ld_d = _rows(call, "d_rows", d_rows, types, shape, dev)
+    rc = lib().moe_combine_bwd(d_out.data_ptr(), ld_o, rows.data_ptr(), ld_r, dtype,
+                               _flat(call, "exp2perm", exp2perm, _I32, maps, dev),
+                               _flat(call, "perm2tok", perm2tok, _I32, (R,), dev),
+                               _flat(call, "total_rows", total_rows, _I32, (1,), dev),
+                               _flat(call, "topk_weights", topk_weights, _F32, maps, dev), T, K, R, H,
+                               d_rows.data_ptr(), ld_d, _flat(call, "d_weights", d_weights, _F32, maps, dev), st)
+    if rc:
+        _check(rc, call)
