@@ -176,20 +176,24 @@ __global__ void __launch_bounds__(64 * kSkWaves) mx_gemm_skinny_kernel(MgArgs a)
 // padding, which the direct copies do not allow; the 16-byte chunks of a row
 // are XOR-permuted so that 16 consecutive rows' reads of one chunk spread over
 // all 64 banks.
-template <int FA, int FW, int MW, int NW>
+template <int FA, int FW, int MW, int NW, bool ALIGNED>
 struct MgShape {
     static constexpr int kBM = 64 * MW, kBN = 64 * NW;
     static constexpr int kElems = FA == MOE_MX_E2M1 ? 256 : 128, kSteps = kElems / 64;    // K of a stage
     static constexpr int kABytes = 128, kWBytes = FW == MOE_MX_E2M1 ? kElems / 2 : kElems;
-    static constexpr int kSf = kElems / 32;                                               // scale bytes of a row
+    // a row's scales in LDS: their bytes, or a word each where they are not aligned
+    static constexpr int kSf = kElems / 32, kSfRow = ALIGNED ? kSf : 4 * kSf;
     static constexpr int kACopies = kBM * kABytes / 4096, kWCopies = kBN * kWBytes / 4096;   // a wave's, per stage
-    static constexpr int kASfCopies = kBM * kSf / 1024 > 0 ? kBM * kSf / 1024 : 1;
-    static constexpr int kWSfCopies = kBN * kSf / 1024 > 0 ? kBN * kSf / 1024 : 1;
-    static constexpr int kW = kBM * kABytes, kASf = kW + kBN * kWBytes, kWSf = kASf + kSf * kBM;
-    static constexpr int kStage = kWSf + kSf * kBN;
-    // as many stages, 2 to 4, as leave a CU 1 (256 x 256), 2 or 3 workgroups
-    static constexpr int kBudget = 160 * 1024 / (MW * NW >= 16 ? 1 : MW * NW >= 4 ? 2 : 3);
-    static constexpr int kRing = 4 * kStage <= kBudget ? 4 : 3 * kStage <= kBudget ? 3 : 2;
+    static constexpr int kASfCopies = kBM * kSfRow / 1024 > 0 ? kBM * kSfRow / 1024 : 1;
+    static constexpr int kWSfCopies = kBN * kSfRow / 1024 > 0 ? kBN * kSfRow / 1024 : 1;
+    static constexpr int kAll = kACopies + kWCopies + kASfCopies + kWSfCopies;
+    static constexpr int kW = kBM * kABytes, kASf = kW + kBN * kWBytes, kWSf = kASf + kSfRow * kBM;
+    static constexpr int kStage = kWSf + kSfRow * kBN;
+    // as many stages, 2 to 6, as leave a CU 1 (256 x 256) or 2 workgroups: what
+    // is in flight hides the memory's latency where the blocks are small
+    static constexpr int kBudget = 160 * 1024 / (MW * NW >= 16 ? 1 : 2);
+    static constexpr int kRing = kBudget / kStage < 6 ? kBudget / kStage : 6;
+    static_assert(kRing >= 2 && (kRing - 1) * kAll < 64, "ring of stages");
 };
 
 template <int BYTES>
@@ -198,7 +202,7 @@ __device__ __forceinline__ int mg_swizzle(int chunk, int row) {
     else return chunk ^ ((row >> 2) & 3);
 }
 
-// Direct-to-LDS load of 4 bytes a lane, as lds_copy16.
+// Direct-to-LDS loads of 4 bytes, or of one byte into a word, a lane, as lds_copy16.
 __device__ __forceinline__ void lds_copy4(u32x4 rsrc, uint32_t lds, uint32_t voff, uint32_t soff) {
     asm volatile("buffer_load_dword %0, %1, %2 offen lds" :: "v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds) : "memory");
 }
@@ -231,19 +235,23 @@ struct MgCopy {
     }
 };
 
-// One operand's scales where a row's are whole aligned words (K / 32 a multiple
-// of 4): SF bytes of each of ROWS rows a stage, one word a lane. Blocks of few
-// rows take less than one instruction a wave: waves then repeat each other's,
-// so that all count alike.
-template <int SF, int ROWS, int COPIES>
+__device__ __forceinline__ void lds_copy1(u32x4 rsrc, uint32_t lds, uint32_t voff, uint32_t soff) {
+    asm volatile("buffer_load_ubyte %0, %1, %2 offen lds" :: "v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds) : "memory");
+}
+
+// One operand's scales: SF bytes of each of ROWS rows a stage. Where a row's
+// scales are whole aligned words (K / 32 a multiple of 4) a lane copies a word,
+// else one byte. Blocks of few rows take less than one instruction a wave:
+// waves then repeat each other's, so that all count alike.
+template <int SF, int ROWS, int COPIES, bool ALIGNED>
 struct MgScaleCopy {
-    static constexpr int kWords = SF / 4, kRowsPer = 64 / kWords, kParts = ROWS / kRowsPer;
+    static constexpr int kEach = ALIGNED ? 4 : 1, kWords = SF / kEach, kRowsPer = 64 / kWords, kParts = ROWS / kRowsPer;
     u32x4 rsrc;
     uint32_t off[COPIES];
     int word;
     __device__ __forceinline__ void init(const uint8_t* base, int nb, int rows_left, int wave, int lane) {
         rsrc = buffer_desc(base);
-        word = 4 * (lane % kWords);
+        word = kEach * (lane % kWords);
 #pragma unroll
         for (int q = 0; q < COPIES; ++q) {
             const int r = kRowsPer * ((4 * q + wave) % kParts) + lane / kWords;
@@ -251,8 +259,10 @@ struct MgScaleCopy {
         }
     }
     __device__ __forceinline__ void issue(uint32_t lds, int s, int q, int wave, int nb) const {
-        lds_copy4(rsrc, __builtin_amdgcn_readfirstlane(lds + (4 * q + wave) % kParts * 256),
-                  s * SF + word < nb ? off[q] : 0x80000000u, (uint32_t)(s * SF));
+        const uint32_t to = __builtin_amdgcn_readfirstlane(lds + (4 * q + wave) % kParts * 256);
+        const uint32_t from = s * SF + word < nb ? off[q] : 0x80000000u;
+        if constexpr (ALIGNED) lds_copy4(rsrc, to, from, (uint32_t)(s * SF));
+        else lds_copy1(rsrc, to, from, (uint32_t)(s * SF));
     }
 };
 
@@ -275,23 +285,22 @@ __device__ __forceinline__ MxFrag<FMT> mg_read(const uint8_t* rows, int row, int
 
 template <int FA, int FW, int MW, int NW, bool ALIGNED, bool F32>
 __global__ void __launch_bounds__(256, MW * NW >= 16 ? 1 : 2) mx_gemm_tiled_kernel(MgArgs a) {
-    using S = MgShape<FA, FW, MW, NW>;
+    using S = MgShape<FA, FW, MW, NW, ALIGNED>;
     constexpr int kOutRow = 32 * NW * (F32 ? 4 : 2) + 16;       // one token's columns of a wave in the epilogue
     constexpr int kLds = S::kRing * S::kStage > 4 * 32 * kOutRow ? S::kRing * S::kStage : 4 * 32 * kOutRow;
-    constexpr int kCodeCopies = S::kACopies + S::kWCopies;
-    constexpr int kAll = kCodeCopies + (ALIGNED ? S::kASfCopies + S::kWSfCopies : 0);
+    constexpr int kCodeCopies = S::kACopies + S::kWCopies, kAll = S::kAll;
     __shared__ __align__(16) uint8_t lds[kLds];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 31, g = lane >> 5, wm = wave >> 1, wn = wave & 1;
 
     // Blocks of the output to workgroups: each XCD (workgroups are dealt to the 8
     // round robin) gets a contiguous run of them, and a run goes through groups
-    // of 8 rows of blocks column by column, so that an XCD's L2 holds what its
-    // workgroups share.
+    // of 4 rows of blocks column by column, so that an XCD's L2 holds what its
+    // workgroups share (4096 x 4096 x 4096 e2m1: 44.9 us with 8 rows, 43.4 with 4).
     const int mt = (a.T + S::kBM - 1) / S::kBM, nt = (a.N + S::kBN - 1) / S::kBN, tiles = mt * nt;
     const int x = blockIdx.x & 7, per = tiles >> 3, more = tiles & 7;
     const int id = x * per + (x < more ? x : more) + (int)(blockIdx.x >> 3);
-    const int group = id / (8 * nt), gm0 = group * 8, gh = mt - gm0 < 8 ? mt - gm0 : 8, in = id - gm0 * nt;
+    const int gm0 = id / (4 * nt) * 4, gh = mt - gm0 < 4 ? mt - gm0 : 4, in = id - gm0 * nt;
     const int64_t m0 = (int64_t)(gm0 + in % gh) * S::kBM, n0 = (int64_t)(in / gh) * S::kBN;
 
     const int nb = a.K >> 5, a_row = (int)mx_bytes(a.K, FA), w_row = (int)mx_bytes(a.K, FW);
@@ -299,14 +308,12 @@ __global__ void __launch_bounds__(256, MW * NW >= 16 ? 1 : 2) mx_gemm_tiled_kern
     const int rows_m = (int)(a.T - m0 < S::kBM ? a.T - m0 : S::kBM), rows_n = (int)(a.N - n0 < S::kBN ? a.N - n0 : S::kBN);
     MgCopy<S::kABytes, S::kACopies> ca;
     MgCopy<S::kWBytes, S::kWCopies> cw;
-    MgScaleCopy<S::kSf, S::kBM, S::kASfCopies> csa;
-    MgScaleCopy<S::kSf, S::kBN, S::kWSfCopies> csw;
+    MgScaleCopy<S::kSf, S::kBM, S::kASfCopies, ALIGNED> csa;
+    MgScaleCopy<S::kSf, S::kBN, S::kWSfCopies, ALIGNED> csw;
     ca.init(a.a + m0 * a_row, a_row, rows_m, wave, lane);
     cw.init(a.w + n0 * w_row, w_row, rows_n, wave, lane);
-    if constexpr (ALIGNED) {
-        csa.init(a.a_sf + m0 * nb, nb, rows_m, wave, lane);
-        csw.init(a.w_sf + n0 * nb, nb, rows_n, wave, lane);
-    }
+    csa.init(a.a_sf + m0 * nb, nb, rows_m, wave, lane);
+    csw.init(a.w_sf + n0 * nb, nb, rows_n, wave, lane);
     const uint32_t lds0 = lds_addr(lds);
     auto copy = [&](int s, int q0, int q1) {        // instructions [q0, q1) of stage s's kAll
         const uint32_t at = lds0 + (s % S::kRing) * S::kStage;
@@ -318,34 +325,24 @@ __global__ void __launch_bounds__(256, MW * NW >= 16 ? 1 : 2) mx_gemm_tiled_kern
             else csw.issue(at + S::kWSf, s, q - kCodeCopies - S::kASfCopies, wave, nb);
         }
     };
-    // scales from global memory (K / 32 not a multiple of 4): row pointers
-    const uint8_t *pa_sf[MW], *pw_sf[NW];
-    if constexpr (!ALIGNED) {
-#pragma unroll
-        for (int m = 0; m < MW; ++m) {
-            const int t = 32 * (wm * MW + m) + r;
-            pa_sf[m] = a.a_sf + (m0 + (t < rows_m ? t : rows_m - 1)) * nb;
+    // a stage's scales of one of the lane's rows: of 4 steps, those of group g's
+    // 4 blocks, step s's in byte s; of 2, blocks g and 2 + g in bytes 0 and 2
+    auto scale = [&](const uint8_t* at, int row) -> uint32_t {
+        if constexpr (ALIGNED) {
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(at + S::kSf * row + (S::kSteps == 4 ? 4 * g : 0));
+            return S::kSteps == 4 ? v : v >> (8 * g);
+        } else {
+            const uint4 v = *reinterpret_cast<const uint4*>(at + S::kSfRow * row + (S::kSteps == 4 ? 16 * g : 0));
+            if constexpr (S::kSteps == 4) return v.x | (v.y << 8) | (v.z << 16) | (v.w << 24);
+            return g ? v.y | (v.w << 16) : v.x | (v.z << 16);
         }
-#pragma unroll
-        for (int n = 0; n < NW; ++n) {
-            const int c = 32 * (wn * NW + n) + r;
-            pw_sf[n] = a.w_sf + (n0 + (c < rows_n ? c : rows_n - 1)) * nb;
-        }
-    }
-    // a stage's scales of one of the lane's rows: the word of group g's 4 blocks,
-    // step s's in byte s; of 2 steps, the stage's word moved so that it is byte 2 s
-    auto scale = [&](int s, const uint8_t* at, const uint8_t* row_sf, int row) {
-        const int w = S::kSteps == 4 ? 4 * g : 0;
-        const uint32_t v = ALIGNED ? *reinterpret_cast<const uint32_t*>(at + S::kSf * row + w)
-                                   : scale_word<false>(row_sf, S::kSf * s + w, nb);
-        return S::kSteps == 4 ? v : v >> (8 * g);
     };
     auto scales = [&](int s, uint32_t (&sa)[MW], uint32_t (&sw)[NW]) {
         const uint8_t* at = lds + (s % S::kRing) * S::kStage;
 #pragma unroll
-        for (int m = 0; m < MW; ++m) sa[m] = scale(s, at + S::kASf, pa_sf[m], 32 * (wm * MW + m) + r);
+        for (int m = 0; m < MW; ++m) sa[m] = scale(at + S::kASf, 32 * (wm * MW + m) + r);
 #pragma unroll
-        for (int n = 0; n < NW; ++n) sw[n] = scale(s, at + S::kWSf, pw_sf[n], 32 * (wn * NW + n) + r);
+        for (int n = 0; n < NW; ++n) sw[n] = scale(at + S::kWSf, 32 * (wn * NW + n) + r);
     };
     struct Operands {
         MxFrag<FA> a[MW];
@@ -384,14 +381,12 @@ __global__ void __launch_bounds__(256, MW * NW >= 16 ? 1 : 2) mx_gemm_tiled_kern
 #pragma unroll
     for (int s = 0; s < S::kRing; ++s) copy(s, 0, kAll);
     Operands o0, o1;
-    if constexpr (!ALIGNED) scales(0, sa, sw);
     __builtin_amdgcn_s_waitcnt(vmcnt_at_most((S::kRing - 1) * kAll));
     __syncthreads();
-    if constexpr (ALIGNED) scales(0, sa, sw);
+    scales(0, sa, sw);
     read(0, 0, o0);
     for (int s = 0; s < stages; ++s) {
         read(s, 1, o1);
-        if constexpr (!ALIGNED) scales(s + 1, sa1, sw1);
         mfmas(o0, std::integral_constant<int, 0>());
         if constexpr (S::kSteps == 4) {
             read(s, 2, o0);
@@ -402,7 +397,7 @@ __global__ void __launch_bounds__(256, MW * NW >= 16 ? 1 : 2) mx_gemm_tiled_kern
         __builtin_amdgcn_s_waitcnt(vmcnt_at_most((S::kRing - 2) * kAll) & lgkmcnt_zero());
         asm volatile("s_barrier" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (ALIGNED) scales(s + 1, sa1, sw1);
+        scales(s + 1, sa1, sw1);
         read(s + 1, 0, o0);
 #pragma unroll
         for (int m = 0; m < MW; ++m) {
@@ -449,7 +444,11 @@ __global__ void __launch_bounds__(256, MW * NW >= 16 ? 1 : 2) mx_gemm_tiled_kern
             const uint8_t* src = slab + tr * kOutRow + c * kEs;
             uint8_t* dst = (uint8_t*)a.out + (t * a.out_stride + n) * kEs;
             if (a.out_vec && n + kPiece <= a.N) {
-                *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
+                // outputs of 256-wide blocks are past what the L2 keeps for a reader:
+                // non-temporal stores (4096 x 4096 x 4096 e2m1: 43.4 -> 42.6 us)
+                const u32x4 v = *reinterpret_cast<const u32x4*>(src);
+                if constexpr (MW * NW >= 16) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(dst));
+                else *reinterpret_cast<u32x4*>(dst) = v;
             } else {
                 for (int e = 0; e < kPiece && n + e < a.N; ++e) {
                     if constexpr (F32) reinterpret_cast<float*>(dst)[e] = reinterpret_cast<const float*>(src)[e];
