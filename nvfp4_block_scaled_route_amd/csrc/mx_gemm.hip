@@ -176,35 +176,53 @@ __global__ void __launch_bounds__(64 * kSkWaves) mx_gemm_skinny_kernel(MgArgs a)
 // padding, which the direct copies do not allow; the 16-byte chunks of a row
 // are XOR-permuted so that 16 consecutive rows' reads of one chunk spread over
 // all 64 banks.
+// A row's scales travel in chunks: 32 of them (1024 elements) as two 16-byte
+// pieces where their words are aligned (K / 32 a multiple of 4, at least 16),
+// else 16 as one byte a lane, each into a word. Every stage's own few bytes
+// would touch as many cache lines as the codes do.
+// PIECES: of an aligned chunk.
+template <int PIECES, bool ALIGNED>
+struct MgScale {
+    static constexpr int kBytes = ALIGNED ? 16 * PIECES : 16, kRow = ALIGNED ? 16 * PIECES : 64;      // of a row, in memory and in LDS
+};
+
 template <int FA, int FW, int MW, int NW, bool ALIGNED>
 struct MgShape {
     static constexpr int kBM = 64 * MW, kBN = 64 * NW;
-    static constexpr int kElems = FA == MOE_MX_E2M1 ? 256 : 128, kSteps = kElems / 64;    // K of a stage
-    static constexpr int kABytes = 128, kWBytes = FW == MOE_MX_E2M1 ? kElems / 2 : kElems;
-    // a row's scales in LDS: their bytes, or a word each where they are not aligned
-    static constexpr int kSf = kElems / 32, kSfRow = ALIGNED ? kSf : 4 * kSf;
+    // K of a stage: 256 where an operand is e2m1 (128 bytes of its rows), but for
+    // 256 x 256 blocks with e4m3 tokens, which LDS does not hold twice
+    static constexpr int kElems = FA == MOE_MX_E2M1 || (FW == MOE_MX_E2M1 && MW * NW < 16) ? 256 : 128;
+    static constexpr int kSteps = kElems / 64;
+    static constexpr int kABytes = FA == MOE_MX_E2M1 ? kElems / 2 : kElems;
+    static constexpr int kWBytes = FW == MOE_MX_E2M1 ? kElems / 2 : kElems;
     static constexpr int kACopies = kBM * kABytes / 4096, kWCopies = kBN * kWBytes / 4096;   // a wave's, per stage
-    static constexpr int kASfCopies = kBM * kSfRow / 1024 > 0 ? kBM * kSfRow / 1024 : 1;
-    static constexpr int kWSfCopies = kBN * kSfRow / 1024 > 0 ? kBN * kSfRow / 1024 : 1;
-    static constexpr int kAll = kACopies + kWCopies + kASfCopies + kWSfCopies;
-    static constexpr int kW = kBM * kABytes, kASf = kW + kBN * kWBytes, kWSf = kASf + kSfRow * kBM;
-    static constexpr int kStage = kWSf + kSfRow * kBN;
-    // as many stages, 2 to 6, as leave a CU 1 (256 x 256) or 2 workgroups: what
-    // is in flight hides the memory's latency where the blocks are small
-    static constexpr int kBudget = 160 * 1024 / (MW * NW >= 16 ? 1 : 2);
-    static constexpr int kRing = kBudget / kStage < 6 ? kBudget / kStage : 6;
+    static constexpr int kAll = kACopies + kWCopies;
+    static constexpr int kW = kBM * kABytes, kStage = kW + kBN * kWBytes;
+    static constexpr int kPieces = MW * NW < 16 || FA == MOE_MX_E2M1 ? 2 : 1;
+    using Sf = MgScale<kPieces, ALIGNED>;
+    static constexpr int kChunk = (kBM + kBN) * Sf::kRow;     // scales, two buffers of kSpc stages each
+    static constexpr int kSpc = Sf::kBytes * 32 / kElems;
+    // as many stages, 2 to 6, as leave a CU 2 workgroups (1 of the widest): what
+    // is in flight hides the memory's latency where the blocks are small. A chunk
+    // of scales overwrites the last but one, whose stages must be past (ring of
+    // at most kSpc + 1).
+    static constexpr int kPerCu = MW * NW >= 8 || 2 * (2 * kStage + 2 * kChunk) > 160 * 1024 ? 1 : 2;
+    static constexpr int kFit = (160 * 1024 / kPerCu - 2 * kChunk) / kStage, kMax = kSpc + 1 < 6 ? kSpc + 1 : 6;
+    static constexpr int kRing = kFit < kMax ? kFit : kMax;
+    static constexpr int kSf = kRing * kStage, kLds = kSf + 2 * kChunk;
     static_assert(kRing >= 2 && (kRing - 1) * kAll < 64, "ring of stages");
 };
 
 template <int BYTES>
 __device__ __forceinline__ int mg_swizzle(int chunk, int row) {
-    if constexpr (BYTES == 128) return chunk ^ (row & 7) ^ ((row >> 3) & 1);
+    if constexpr (BYTES == 256) return chunk ^ (row & 15);
+    else if constexpr (BYTES == 128) return chunk ^ (row & 7) ^ ((row >> 3) & 1);
     else return chunk ^ ((row >> 2) & 3);
 }
 
-// Direct-to-LDS loads of 4 bytes, or of one byte into a word, a lane, as lds_copy16.
-__device__ __forceinline__ void lds_copy4(u32x4 rsrc, uint32_t lds, uint32_t voff, uint32_t soff) {
-    asm volatile("buffer_load_dword %0, %1, %2 offen lds" :: "v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds) : "memory");
+// Direct-to-LDS load of one byte a lane into a word, as lds_copy16.
+__device__ __forceinline__ void lds_copy1(u32x4 rsrc, uint32_t lds, uint32_t voff, uint32_t soff) {
+    asm volatile("buffer_load_ubyte %0, %1, %2 offen lds" :: "v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds) : "memory");
 }
 
 // One operand's codes: instruction q of a wave copies 1 KB, the rows
@@ -235,47 +253,45 @@ struct MgCopy {
     }
 };
 
-__device__ __forceinline__ void lds_copy1(u32x4 rsrc, uint32_t lds, uint32_t voff, uint32_t soff) {
-    asm volatile("buffer_load_ubyte %0, %1, %2 offen lds" :: "v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds) : "memory");
-}
-
-// One operand's scales: SF bytes of each of ROWS rows a stage. Where a row's
-// scales are whole aligned words (K / 32 a multiple of 4) a lane copies a word,
-// else one byte. Blocks of few rows take less than one instruction a wave:
-// waves then repeat each other's, so that all count alike.
-template <int SF, int ROWS, int COPIES, bool ALIGNED>
+// One operand's scales. Blocks of few rows take less than one instruction a
+// wave: waves then repeat each other's.
+template <int ROWS, int PIECES, bool ALIGNED>
 struct MgScaleCopy {
-    static constexpr int kEach = ALIGNED ? 4 : 1, kWords = SF / kEach, kRowsPer = 64 / kWords, kParts = ROWS / kRowsPer;
+    static constexpr int kLanes = ALIGNED ? PIECES : 16, kRowsPer = 64 / kLanes, kParts = ROWS / kRowsPer;
+    static constexpr int kCopies = kParts > 4 ? kParts / 4 : 1;
     u32x4 rsrc;
-    uint32_t off[COPIES];
-    int word;
+    uint32_t off[kCopies];  // of a lane's rows
     __device__ __forceinline__ void init(const uint8_t* base, int nb, int rows_left, int wave, int lane) {
         rsrc = buffer_desc(base);
-        word = kEach * (lane % kWords);
 #pragma unroll
-        for (int q = 0; q < COPIES; ++q) {
-            const int r = kRowsPer * ((4 * q + wave) % kParts) + lane / kWords;
-            off[q] = (uint32_t)((r < rows_left ? r : rows_left - 1) * nb + word);
+        for (int q = 0; q < kCopies; ++q) {
+            const int r = kRowsPer * ((4 * q + wave) % kParts) + lane / kLanes;
+            off[q] = (uint32_t)((r < rows_left ? r : rows_left - 1) * nb);
         }
     }
-    __device__ __forceinline__ void issue(uint32_t lds, int s, int q, int wave, int nb) const {
-        const uint32_t to = __builtin_amdgcn_readfirstlane(lds + (4 * q + wave) % kParts * 256);
-        const uint32_t from = s * SF + word < nb ? off[q] : 0x80000000u;
-        if constexpr (ALIGNED) lds_copy4(rsrc, to, from, (uint32_t)(s * SF));
-        else lds_copy1(rsrc, to, from, (uint32_t)(s * SF));
+    // Chunk c into LDS at lds. The piece that would pass the row's end lies
+    // against it instead (mg_scales goes by that); bytes behind it are zeros.
+    __device__ __forceinline__ void issue(uint32_t lds, int c, int wave, int lane, int nb) const {
+        const int b = ALIGNED ? 16 * (PIECES * c + lane % PIECES) : 16 * c + lane % 16;
+        const int at = !ALIGNED ? b : b < nb - 16 ? b : nb - 16;
+#pragma unroll
+        for (int q = 0; q < kCopies; ++q) {
+            const uint32_t to = __builtin_amdgcn_readfirstlane(lds + (4 * q + wave) % kParts * (ALIGNED ? 1024 : 256));
+            if constexpr (ALIGNED) lds_copy16(rsrc, to, off[q] + at, 0u);
+            else lds_copy1(rsrc, to, b < nb ? off[q] + at : 0x80000000u, 0u);
+        }
     }
 };
 
-// A lane's operand of a step: e2m1, one block (of 4 steps: block 4 g + step, so
-// that a group's scales are one word; of 2: block 2 step + g, e4m3's order);
-// e4m3, its share of blocks 2 step and 2 step + 1.
-template <int FMT, int BYTES, int STEPS>
+// A lane's operand of a step. e2m1: one block, block 4 g + step of the stage (so
+// that a group's scales are one word), or beside e4m3 (PAIR) block 2 step + g,
+// e4m3's order; e4m3: its share of blocks 2 step and 2 step + 1.
+template <int FMT, int BYTES, bool PAIR>
 __device__ __forceinline__ MxFrag<FMT> mg_read(const uint8_t* rows, int row, int g, int step) {
     MxFrag<FMT> f;
     const uint8_t* p = rows + row * BYTES;
     if constexpr (FMT == MOE_MX_E2M1) {
-        const int c = STEPS == 4 ? 4 * g + step : 2 * step + g;
-        f.q[0] = *reinterpret_cast<const uint4*>(p + 16 * mg_swizzle<BYTES>(c, row));
+        f.q[0] = *reinterpret_cast<const uint4*>(p + 16 * mg_swizzle<BYTES>(PAIR ? 2 * step + g : 4 * g + step, row));
     } else {
         f.q[0] = *reinterpret_cast<const uint4*>(p + 16 * mg_swizzle<BYTES>(4 * step + g, row));
         f.q[1] = *reinterpret_cast<const uint4*>(p + 16 * mg_swizzle<BYTES>(4 * step + 2 + g, row));
@@ -283,12 +299,39 @@ __device__ __forceinline__ MxFrag<FMT> mg_read(const uint8_t* rows, int row, int
     return f;
 }
 
+// The scales of blocks [b, b + 4) of a row in LDS, a byte each, zeros behind the
+// row's nb.
+template <int PIECES, bool ALIGNED>
+__device__ __forceinline__ uint32_t mg_scale_word(const uint8_t* row, int b, int nb) {
+    if constexpr (ALIGNED) {
+        const int piece = b & ~15, at = piece < nb - 16 ? piece : nb - 16;
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(row + (PIECES == 2 ? b & 16 : 0) + (b < nb ? b - at : 0));
+        return b < nb ? v : 0u;
+    } else {
+        const uint4 v = *reinterpret_cast<const uint4*>(row + (b & 15) * 4);
+        return v.x | (v.y << 8) | (v.z << 16) | (v.w << 24);
+    }
+}
+
+// A stage's scales of a lane's row as one register: step s's in byte s, or with 2
+// steps in byte 2 s. b0: the stage's first block.
+template <int STEPS, bool PAIR, int PIECES, bool ALIGNED>
+__device__ __forceinline__ uint32_t mg_scales(const uint8_t* row, int b0, int nb, int g) {
+    if constexpr (!PAIR) return mg_scale_word<PIECES, ALIGNED>(row, b0 + 4 * g, nb);        // blocks 4 g + step
+    const uint32_t v = mg_scale_word<PIECES, ALIGNED>(row, b0, nb);
+    if constexpr (STEPS == 2) return v >> (8 * g);                                  // blocks g, 2 + g
+    const uint32_t w = mg_scale_word<PIECES, ALIGNED>(row, b0 + 4, nb);                     // and 4 + g, 6 + g
+    return __builtin_amdgcn_perm(w, v, g ? 0x07050301u : 0x06040200u);
+}
+
 template <int FA, int FW, int MW, int NW, bool ALIGNED, bool F32>
-__global__ void __launch_bounds__(256, MW * NW >= 16 ? 1 : 2) mx_gemm_tiled_kernel(MgArgs a) {
+__global__ void __launch_bounds__(256, (MgShape<FA, FW, MW, NW, ALIGNED>::kPerCu)) mx_gemm_tiled_kernel(MgArgs a) {
     using S = MgShape<FA, FW, MW, NW, ALIGNED>;
     constexpr int kOutRow = 32 * NW * (F32 ? 4 : 2) + 16;       // one token's columns of a wave in the epilogue
-    constexpr int kLds = S::kRing * S::kStage > 4 * 32 * kOutRow ? S::kRing * S::kStage : 4 * 32 * kOutRow;
-    constexpr int kCodeCopies = S::kACopies + S::kWCopies, kAll = S::kAll;
+    constexpr int kLds = S::kLds > 4 * 32 * kOutRow ? S::kLds : 4 * 32 * kOutRow;
+    constexpr bool kPair = FA == MOE_MX_E4M3;
+    using Sf = typename S::Sf;
+    constexpr int kAll = S::kAll;
     __shared__ __align__(16) uint8_t lds[kLds];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 31, g = lane >> 5, wm = wave >> 1, wn = wave & 1;
@@ -308,41 +351,35 @@ __global__ void __launch_bounds__(256, MW * NW >= 16 ? 1 : 2) mx_gemm_tiled_kern
     const int rows_m = (int)(a.T - m0 < S::kBM ? a.T - m0 : S::kBM), rows_n = (int)(a.N - n0 < S::kBN ? a.N - n0 : S::kBN);
     MgCopy<S::kABytes, S::kACopies> ca;
     MgCopy<S::kWBytes, S::kWCopies> cw;
-    MgScaleCopy<S::kSf, S::kBM, S::kASfCopies, ALIGNED> csa;
-    MgScaleCopy<S::kSf, S::kBN, S::kWSfCopies, ALIGNED> csw;
+    MgScaleCopy<S::kBM, S::kPieces, ALIGNED> csa;
+    MgScaleCopy<S::kBN, S::kPieces, ALIGNED> csw;
     ca.init(a.a + m0 * a_row, a_row, rows_m, wave, lane);
     cw.init(a.w + n0 * w_row, w_row, rows_n, wave, lane);
     csa.init(a.a_sf + m0 * nb, nb, rows_m, wave, lane);
     csw.init(a.w_sf + n0 * nb, nb, rows_n, wave, lane);
     const uint32_t lds0 = lds_addr(lds);
-    auto copy = [&](int s, int q0, int q1) {        // instructions [q0, q1) of stage s's kAll
+    auto copy = [&](int s, int q0, int q1) {        // instructions [q0, q1) of stage s's kAll codes
+        // a chunk of scales goes before the codes of its first stage: what waits
+        // for those has waited for these
+        if (q0 == 0 && s % S::kSpc == 0) {
+            const uint32_t at = lds0 + S::kSf + (s / S::kSpc & 1) * S::kChunk;
+            csa.issue(at, s / S::kSpc, wave, lane, nb);
+            csw.issue(at + S::kBM * Sf::kRow, s / S::kSpc, wave, lane, nb);
+        }
         const uint32_t at = lds0 + (s % S::kRing) * S::kStage;
 #pragma unroll
         for (int q = q0; q < q1; ++q) {
             if (q < S::kACopies) ca.issue(at, s, q, wave, a_row);
-            else if (q < kCodeCopies) cw.issue(at + S::kW, s, q - S::kACopies, wave, w_row);
-            else if (q < kCodeCopies + S::kASfCopies) csa.issue(at + S::kASf, s, q - kCodeCopies, wave, nb);
-            else csw.issue(at + S::kWSf, s, q - kCodeCopies - S::kASfCopies, wave, nb);
-        }
-    };
-    // a stage's scales of one of the lane's rows: of 4 steps, those of group g's
-    // 4 blocks, step s's in byte s; of 2, blocks g and 2 + g in bytes 0 and 2
-    auto scale = [&](const uint8_t* at, int row) -> uint32_t {
-        if constexpr (ALIGNED) {
-            const uint32_t v = *reinterpret_cast<const uint32_t*>(at + S::kSf * row + (S::kSteps == 4 ? 4 * g : 0));
-            return S::kSteps == 4 ? v : v >> (8 * g);
-        } else {
-            const uint4 v = *reinterpret_cast<const uint4*>(at + S::kSfRow * row + (S::kSteps == 4 ? 16 * g : 0));
-            if constexpr (S::kSteps == 4) return v.x | (v.y << 8) | (v.z << 16) | (v.w << 24);
-            return g ? v.y | (v.w << 16) : v.x | (v.z << 16);
+            else cw.issue(at + S::kW, s, q - S::kACopies, wave, w_row);
         }
     };
     auto scales = [&](int s, uint32_t (&sa)[MW], uint32_t (&sw)[NW]) {
-        const uint8_t* at = lds + (s % S::kRing) * S::kStage;
+        const uint8_t* at = lds + S::kSf + (s / S::kSpc & 1) * S::kChunk;
+        const int b0 = s * (S::kElems / 32);
 #pragma unroll
-        for (int m = 0; m < MW; ++m) sa[m] = scale(at + S::kASf, 32 * (wm * MW + m) + r);
+        for (int m = 0; m < MW; ++m) sa[m] = mg_scales<S::kSteps, kPair, S::kPieces, ALIGNED>(at + Sf::kRow * (32 * (wm * MW + m) + r), b0, nb, g);
 #pragma unroll
-        for (int n = 0; n < NW; ++n) sw[n] = scale(at + S::kWSf, 32 * (wn * NW + n) + r);
+        for (int n = 0; n < NW; ++n) sw[n] = mg_scales<S::kSteps, kPair, S::kPieces, ALIGNED>(at + Sf::kRow * (S::kBM + 32 * (wn * NW + n) + r), b0, nb, g);
     };
     struct Operands {
         MxFrag<FA> a[MW];
@@ -351,9 +388,9 @@ __global__ void __launch_bounds__(256, MW * NW >= 16 ? 1 : 2) mx_gemm_tiled_kern
     auto read = [&](int s, int step, Operands& o) {
         const uint8_t* at = lds + (s % S::kRing) * S::kStage;
 #pragma unroll
-        for (int n = 0; n < NW; ++n) o.w[n] = mg_read<FW, S::kWBytes, S::kSteps>(at + S::kW, 32 * (wn * NW + n) + r, g, step);
+        for (int n = 0; n < NW; ++n) o.w[n] = mg_read<FW, S::kWBytes, kPair>(at + S::kW, 32 * (wn * NW + n) + r, g, step);
 #pragma unroll
-        for (int m = 0; m < MW; ++m) o.a[m] = mg_read<FA, S::kABytes, S::kSteps>(at, 32 * (wm * MW + m) + r, g, step);
+        for (int m = 0; m < MW; ++m) o.a[m] = mg_read<FA, S::kABytes, kPair>(at, 32 * (wm * MW + m) + r, g, step);
     };
 
     mx_f16v acc[MW][NW];
@@ -485,15 +522,19 @@ int launch_mx_gemm(const MgArgs& a, hipStream_t s) {
     const auto tiles = [&](int bm, int bn) { return (int64_t)((a.T + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
     if (tiles(64, 64) > 0x7FFFFFFF) return fail(MOE_EUNSUPPORTED, "%s: too many output tiles", name);
     // the largest tile that still gives every CU one
-    if (tiles(256, 256) >= 192) launch_mx_tiled<FA, FW, 4, 4, ALIGNED>(a, s);
-    else if (tiles(128, 128) >= 192) launch_mx_tiled<FA, FW, 2, 2, ALIGNED>(a, s);
+    if constexpr (ALIGNED)
+        if (tiles(256, 256) >= 192) {
+            launch_mx_tiled<FA, FW, 4, 4, ALIGNED>(a, s);
+            return check_launch(name);
+        }
+    if (tiles(128, 128) >= 192) launch_mx_tiled<FA, FW, 2, 2, ALIGNED>(a, s);
     else launch_mx_tiled<FA, FW, 1, 1, ALIGNED>(a, s);
     return check_launch(name);
 }
 
 template <int FA, int FW>
 int launch_mx_gemm(const MgArgs& a, hipStream_t s) {
-    return (a.K / 32) % 4 == 0 ? launch_mx_gemm<FA, FW, true>(a, s) : launch_mx_gemm<FA, FW, false>(a, s);
+    return (a.K / 32) % 4 == 0 && a.K >= 512 ? launch_mx_gemm<FA, FW, true>(a, s) : launch_mx_gemm<FA, FW, false>(a, s);
 }
 
 }  // namespace moe
