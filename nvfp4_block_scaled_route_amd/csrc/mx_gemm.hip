@@ -74,7 +74,7 @@ __device__ __forceinline__ void store_out(const MgArgs& a, int64_t t, int n, flo
 }
 
 // ------------------------------------------------------------------ few tokens
-// Up to 64 tokens the product is a stream of the weights. A workgroup owns 16
+// Up to 32 tokens the product is a stream of the weights. A workgroup owns 16
 // columns and its 8 waves split K, so that N = 4096 columns already put a
 // workgroup on each CU and all of a column's weights are in flight at once;
 // the waves' sums are added through LDS in wave order. 16 x 16 x 128 MFMAs
@@ -98,7 +98,7 @@ __device__ __forceinline__ MxFrag<FMT> load_frag16(const uint8_t* row, int step,
 
 template <int FA, int FW, int TM, bool ALIGNED>
 __global__ void __launch_bounds__(64 * kSkWaves) mx_gemm_skinny_kernel(MgArgs a) {
-    constexpr int U = TM == 4 ? 2 : 4;      // steps whose loads issue together
+    constexpr int U = 4;                    // steps whose loads issue together
     __shared__ floatx4 s_sum[kSkWaves][TM][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
     const int n0 = blockIdx.x * 16, nb = a.K >> 5;
@@ -190,15 +190,16 @@ template <int FA, int FW, int MW, int NW, bool ALIGNED>
 struct MgShape {
     static constexpr int kBM = 64 * MW, kBN = 64 * NW;
     // K of a stage: 256 where an operand is e2m1 (128 bytes of its rows), but for
-    // 256 x 256 blocks with e4m3 tokens, which LDS does not hold twice
-    static constexpr int kElems = FA == MOE_MX_E2M1 || (FW == MOE_MX_E2M1 && MW * NW < 16) ? 256 : 128;
+    // the wider blocks with e4m3 tokens, of which LDS would hold too few stages
+    // (2048 x 4096 x 4096 in 128-wide blocks: 48.3 us with 256, 41.2 with 128)
+    static constexpr int kElems = FA == MOE_MX_E2M1 || (FW == MOE_MX_E2M1 && MW * NW < 4) ? 256 : 128;
     static constexpr int kSteps = kElems / 64;
     static constexpr int kABytes = FA == MOE_MX_E2M1 ? kElems / 2 : kElems;
     static constexpr int kWBytes = FW == MOE_MX_E2M1 ? kElems / 2 : kElems;
     static constexpr int kACopies = kBM * kABytes / 4096, kWCopies = kBN * kWBytes / 4096;   // a wave's, per stage
     static constexpr int kAll = kACopies + kWCopies;
     static constexpr int kW = kBM * kABytes, kStage = kW + kBN * kWBytes;
-    static constexpr int kPieces = MW * NW < 16 || FA == MOE_MX_E2M1 ? 2 : 1;
+    static constexpr int kPieces = MW * NW < 16 ? 2 : 1;
     using Sf = MgScale<kPieces, ALIGNED>;
     static constexpr int kChunk = (kBM + kBN) * Sf::kRow;     // scales, two buffers of kSpc stages each
     static constexpr int kSpc = Sf::kBytes * 32 / kElems;
@@ -512,22 +513,31 @@ void launch_mx_tiled(const MgArgs& a, hipStream_t s) {
 template <int FA, int FW, bool ALIGNED>
 int launch_mx_gemm(const MgArgs& a, hipStream_t s) {
     const char* name = "mx_gemm";
-    if (a.T <= 64) {
+    // K = N = 4096, e4m3 x e2m1: 32 tokens 9.7 us by columns, 10.6 in 64-wide
+    // blocks; 64 tokens 15.6 and 11.0
+    if (a.T <= 32) {
         const dim3 g((unsigned)((a.N + 15) / 16)), b(64 * kSkWaves);
         if (a.T <= 16) hipLaunchKernelGGL((mx_gemm_skinny_kernel<FA, FW, 1, ALIGNED>), g, b, 0, s, a);
-        else if (a.T <= 32) hipLaunchKernelGGL((mx_gemm_skinny_kernel<FA, FW, 2, ALIGNED>), g, b, 0, s, a);
-        else hipLaunchKernelGGL((mx_gemm_skinny_kernel<FA, FW, 4, ALIGNED>), g, b, 0, s, a);
+        else hipLaunchKernelGGL((mx_gemm_skinny_kernel<FA, FW, 2, ALIGNED>), g, b, 0, s, a);
         return check_launch(name);
     }
     const auto tiles = [&](int bm, int bn) { return (int64_t)((a.T + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
     if (tiles(64, 64) > 0x7FFFFFFF) return fail(MOE_EUNSUPPORTED, "%s: too many output tiles", name);
-    // the largest tile that still gives every CU one
-    if constexpr (ALIGNED)
-        if (tiles(256, 256) >= 192) {
+    // The widest block that fills the chip: wide blocks read less per product,
+    // but a CU without one idles. us with K = 4096 (64 x 64, 64 x 128, 128 x 128,
+    // 256 x 256):
+    //   517 x 2048 e4m3 x e2m1   16.0  16.9  28.4  53.6     1024 x 4096  30.0  23.0  29.9  53.8
+    //   1536 x 4096 e4m3 x e2m1  43.8  36.1  32.9  54.1     2048 x 4096  57.2  42.9  37.3  53.8
+    //   1536 x 4096 e2m1         31.9  28.6  22.7  36.6     2800 x 4096  55.4  46.5  38.5  37.6
+    // (rows of scales that are not aligned leave LDS for blocks up to 128 x 128)
+    if constexpr (ALIGNED) {
+        if (tiles(256, 256) >= 168) {
             launch_mx_tiled<FA, FW, 4, 4, ALIGNED>(a, s);
             return check_launch(name);
         }
-    if (tiles(128, 128) >= 192) launch_mx_tiled<FA, FW, 2, 2, ALIGNED>(a, s);
+    }
+    if (tiles(128, 128) >= 320) launch_mx_tiled<FA, FW, 2, 2, ALIGNED>(a, s);
+    else if (tiles(64, 64) > 512) launch_mx_tiled<FA, FW, 1, 2, ALIGNED>(a, s);
     else launch_mx_tiled<FA, FW, 1, 1, ALIGNED>(a, s);
     return check_launch(name);
 }

@@ -203,6 +203,23 @@ def test_gemm_larger_tiles(T, Nn, K, af, wf):
     _check_gemm(T, Nn, K, af, wf)
 
 
+@pytest.mark.parametrize("af,wf", FORMATS)
+@pytest.mark.parametrize("T,Nn", [(130, 200), (1030, 2200), (1700, 3300), (2817, 3841)])
+@pytest.mark.parametrize("K", [512, 640, 1152])
+def test_gemm_each_block_size(T, Nn, K, af, wf):
+    """Blocks of 64 x 64, 64 x 128, 128 x 128 and 256 x 256 with aligned scales:
+    K of whole chunks of scales, cut ones, and one piece over."""
+    _check_gemm(T, Nn, K, af, wf)
+
+
+@pytest.mark.parametrize("af,wf", FORMATS)
+@pytest.mark.parametrize("K", [1024, 1056, 2176, 4128, 8320])
+def test_gemm_many_stages(K, af, wf):
+    """Rings and chunks of scales that wrap round many times."""
+    _check_gemm(100, 150, K, af, wf)
+    _check_gemm(33, 64, K, af, wf)
+
+
 @pytest.mark.parametrize("T", [5, 40, 90])
 def test_gemm_special_scales(T):
     """NaN scales make their token's row or their column NaN and nothing else,
