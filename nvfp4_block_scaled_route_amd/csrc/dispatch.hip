@@ -58,13 +58,16 @@ __device__ __forceinline__ int64_t route_row(const int32_t* exp2perm, int64_t ro
 // whole tiles of the rows, the weights' gradients among them, are the routes'
 // alone. Rows from total_rows on are left as they were.
 __device__ __forceinline__ void zero_padding(const SortArgs& a, int64_t group) {
-    const int64_t total = *a.total_rows, p0 = group * kPadRows;
-    for (int i = 0; i < kPadRows; ++i) {
-        const int64_t p = p0 + i;
-        if (p >= a.R || p >= total) break;
-        if (a.perm2tok[p] >= 0) continue;
-        for (int u = threadIdx.x; u < a.units; u += blockDim.x)
-            store16(a.rows + p * a.rows_stride + (int64_t)u * 16, make_uint4(0u, 0u, 0u, 0u));
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int64_t total = *a.total_rows, p0 = group * kPadRows, p = p0 + lane;
+    // one load looks at the group's rows, a wave then takes every waves-th
+    bool empty = false;
+    if (lane < kPadRows && p < a.R && p < total) empty = a.perm2tok[p] < 0;
+    uint64_t rows = __ballot(empty);
+    for (int n = 0; rows; ++n, rows &= rows - 1) {
+        if (n % waves != wave) continue;
+        uint8_t* row = a.rows + (p0 + __builtin_ctzll(rows)) * a.rows_stride;
+        for (int u = lane; u < a.units; u += 64) store16(row + (int64_t)u * 16, make_uint4(0u, 0u, 0u, 0u));
     }
 }
 

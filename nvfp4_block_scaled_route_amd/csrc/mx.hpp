@@ -94,13 +94,13 @@ __device__ __forceinline__ uint32_t amax8_bits(const float (&v)[8]) {
 }
 
 // Lane's 8 values (a quad holds one block, in order) -> codes and scale byte at
-// octet `oct` of a row whose code and scale rows start at codes and sf.
+// octet `oct` from codes and sf on.
 template <int FMT>
-__device__ __forceinline__ void mx_store8(const float (&v)[8], int oct, uint8_t* codes, uint8_t* sf) {
+__device__ __forceinline__ void mx_store8(const float (&v)[8], int64_t oct, uint8_t* codes, uint8_t* sf) {
     const uint32_t byte = mx_scale_byte<FMT>(quad_max(amax8_bits(v)));
     const uint2 c = mx_codes8<FMT>(v, byte);
-    if constexpr (FMT == MOE_MX_E2M1) *reinterpret_cast<uint32_t*>(codes + (int64_t)oct * 4) = c.x;
-    else *reinterpret_cast<uint2*>(codes + (int64_t)oct * 8) = c;
+    if constexpr (FMT == MOE_MX_E2M1) *reinterpret_cast<uint32_t*>(codes + oct * 4) = c.x;
+    else *reinterpret_cast<uint2*>(codes + oct * 8) = c;
     if ((oct & 3) == 0) sf[oct >> 2] = (uint8_t)byte;
 }
 

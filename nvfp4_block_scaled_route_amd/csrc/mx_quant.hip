@@ -25,21 +25,38 @@ struct MqArgs {
     uint8_t* sf;
 };
 
-// Octet `first + tid` of the T x H values, row by row: a workgroup finds the
-// row of its first octet once (a uniform 64-bit division), a lane its own by a
-// 32-bit one. first is a multiple of 4 and H of 32, so quads hold whole blocks.
-template <int FMT>
+// Octet i of the T x H values, row by row, in a matrix whose rows lie `stride`
+// elements apart (ROWS: else rows follow one another and i is the place). A
+// workgroup finds the row of its first octet once (a uniform 64-bit division),
+// a lane its own by a 32-bit one. first is a multiple of 4 and H of 32, so quads
+// hold whole blocks.
+template <bool ROWS>
+__device__ __forceinline__ int64_t octet_at(int64_t first, int off, int row_octs, int64_t stride) {
+    if constexpr (!ROWS) return (first + off) * 8;
+    const int64_t row0 = first / row_octs;
+    const uint32_t o = (uint32_t)(first - row0 * row_octs) + (uint32_t)off, dr = o / (uint32_t)row_octs;
+    return (row0 + dr) * stride + (int64_t)(o - dr * (uint32_t)row_octs) * 8;
+}
+
+// U octets a thread, their loads together.
+template <int FMT, bool ROWS, int U>
 __global__ void __launch_bounds__(kMqThreads) mx_quant_kernel(MqArgs a) {
-    const int64_t first = (int64_t)blockIdx.x * kMqThreads;
-    const int64_t row0 = first / a.row_octs;
-    const uint32_t off = (uint32_t)(first - row0 * a.row_octs) + threadIdx.x;
-    if (first + threadIdx.x >= a.octs) return;
-    const uint32_t dr = off / (uint32_t)a.row_octs;
-    const int oct = (int)(off - dr * (uint32_t)a.row_octs);
-    const int64_t t = row0 + dr;
-    float v[8];
-    unpack8(*reinterpret_cast<const uint4*>(a.x + t * a.x_row_stride + (int64_t)oct * 8), v);
-    mx_store8<FMT>(v, oct, a.codes + t * mx_bytes((int64_t)a.row_octs * 8, FMT), a.sf + t * (a.row_octs >> 2));
+    const int64_t first = (int64_t)blockIdx.x * (kMqThreads * U);
+    uint4 raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int off = u * kMqThreads + (int)threadIdx.x;
+        if (first + off < a.octs)
+            raw[u] = *reinterpret_cast<const uint4*>(a.x + octet_at<ROWS>(first, off, a.row_octs, a.x_row_stride));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t i = first + u * kMqThreads + threadIdx.x;
+        if (i >= a.octs) return;
+        float v[8];
+        unpack8(raw[u], v);
+        mx_store8<FMT>(v, i, a.codes, a.sf);
+    }
 }
 
 struct MdArgs {
@@ -51,29 +68,23 @@ struct MdArgs {
     int64_t out_row_stride;
 };
 
-// code * 2^(byte - 127) in fp32 (exact but below 2^-149; the factor of byte 0
-// is the subnormal 2^-127), rounded once to bf16; NaN under byte 255.
-template <int FMT>
+// code * 2^(byte - 127) in fp32 (exact; the factor of byte 0 is the subnormal
+// 2^-127), rounded once to bf16; NaN under byte 255. An octet a thread.
+template <int FMT, bool ROWS>
 __global__ void __launch_bounds__(kMqThreads) mx_dequant_kernel(MdArgs a) {
-    const int64_t first = (int64_t)blockIdx.x * kMqThreads;
-    const int64_t row0 = first / a.row_octs;
-    const uint32_t off = (uint32_t)(first - row0 * a.row_octs) + threadIdx.x;
-    if (first + threadIdx.x >= a.octs) return;
-    const uint32_t dr = off / (uint32_t)a.row_octs;
-    const int oct = (int)(off - dr * (uint32_t)a.row_octs);
-    const int64_t t = row0 + dr, i = first + threadIdx.x;
+    const int64_t first = (int64_t)blockIdx.x * kMqThreads, i = first + threadIdx.x;
+    if (i >= a.octs) return;
     const uint32_t byte = a.sf[i >> 2];
     const float s = byte == 255u ? __uint_as_float(0x7FC00000u)
                                  : byte == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23);
     float v[8];
     if constexpr (FMT == MOE_MX_E2M1) {
         const uint32_t w = *reinterpret_cast<const uint32_t*>(a.codes + i * 4);
+        // the hardware's conversion: e2m1 values are exact in f16
+        const half2v h[4] = {__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0), __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1),
+                             __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2), __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3)};
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {   // magnitude codes 0 .. 7: 0, .5, 1, 1.5, 2, 3, 4, 6
-            const uint32_t c = (w >> (4 * k)) & 15u, e = (c >> 1) & 3u, m = c & 1u;
-            const float mag = e == 0u ? 0.5f * (float)m : __uint_as_float(((e + 126u) << 23) | (m << 22));
-            v[k] = (c & 8u) ? -mag : mag;
-        }
+        for (int k = 0; k < 8; ++k) v[k] = (float)h[k / 2][k % 2];
     } else {
         const uint2 w = *reinterpret_cast<const uint2*>(a.codes + i * 8);
 #pragma unroll
@@ -86,7 +97,18 @@ __global__ void __launch_bounds__(kMqThreads) mx_dequant_kernel(MdArgs a) {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         o[k] = f32_to_bf16(__fmul_rn(v[2 * k], s)) | (f32_to_bf16(__fmul_rn(v[2 * k + 1], s)) << 16);
-    *reinterpret_cast<uint4*>(a.out + t * a.out_row_stride + (int64_t)oct * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(a.out + octet_at<ROWS>(first, threadIdx.x, a.row_octs, a.out_row_stride)) =
+        make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <int FMT, bool ROWS>
+void launch_quant(const MqArgs& a, hipStream_t s) {
+    // two octets a thread once there are eight workgroups a CU of it
+    const dim3 b(kMqThreads);
+    if (a.octs >= 2048LL * 2 * kMqThreads)
+        hipLaunchKernelGGL((mx_quant_kernel<FMT, ROWS, 2>), dim3((unsigned)((a.octs + 2 * kMqThreads - 1) / (2 * kMqThreads))), b, 0, s, a);
+    else
+        hipLaunchKernelGGL((mx_quant_kernel<FMT, ROWS, 1>), dim3((unsigned)((a.octs + kMqThreads - 1) / kMqThreads)), b, 0, s, a);
 }
 
 // ------------------------------------------------------------------ residual + norm + MX
@@ -228,9 +250,9 @@ extern "C" int mx_quant(const uint16_t* x, int64_t x_row_stride, int T, int H, i
     const int rc = mx_check(x, x_row_stride, T, H, fmt, codes, sf, "mx_quant");
     if (rc != MOE_OK || T == 0 || H == 0) return rc;
     MqArgs a{x, x_row_stride, (int64_t)T * (H / 8), H / 8, codes, sf};
-    const dim3 g((unsigned)((a.octs + kMqThreads - 1) / kMqThreads)), b(kMqThreads);
-    if (fmt == MOE_MX_E2M1) hipLaunchKernelGGL(mx_quant_kernel<MOE_MX_E2M1>, g, b, 0, (hipStream_t)stream, a);
-    else hipLaunchKernelGGL(mx_quant_kernel<MOE_MX_E4M3>, g, b, 0, (hipStream_t)stream, a);
+    const bool rows = T > 1 && x_row_stride != H;
+    if (fmt == MOE_MX_E2M1) rows ? launch_quant<MOE_MX_E2M1, true>(a, (hipStream_t)stream) : launch_quant<MOE_MX_E2M1, false>(a, (hipStream_t)stream);
+    else rows ? launch_quant<MOE_MX_E4M3, true>(a, (hipStream_t)stream) : launch_quant<MOE_MX_E4M3, false>(a, (hipStream_t)stream);
     return check_launch("mx_quant");
 }
 
@@ -241,8 +263,12 @@ extern "C" int mx_dequant(const uint8_t* codes, const uint8_t* sf, int T, int H,
     if (rc != MOE_OK || T == 0 || H == 0) return rc;
     MdArgs a{codes, sf, (int64_t)T * (H / 8), H / 8, out, out_row_stride};
     const dim3 g((unsigned)((a.octs + kMqThreads - 1) / kMqThreads)), b(kMqThreads);
-    if (fmt == MOE_MX_E2M1) hipLaunchKernelGGL(mx_dequant_kernel<MOE_MX_E2M1>, g, b, 0, (hipStream_t)stream, a);
-    else hipLaunchKernelGGL(mx_dequant_kernel<MOE_MX_E4M3>, g, b, 0, (hipStream_t)stream, a);
+    hipStream_t st = (hipStream_t)stream;
+    const bool rows = T > 1 && out_row_stride != H;
+    if (fmt == MOE_MX_E2M1 && rows) hipLaunchKernelGGL((mx_dequant_kernel<MOE_MX_E2M1, true>), g, b, 0, st, a);
+    else if (fmt == MOE_MX_E2M1) hipLaunchKernelGGL((mx_dequant_kernel<MOE_MX_E2M1, false>), g, b, 0, st, a);
+    else if (rows) hipLaunchKernelGGL((mx_dequant_kernel<MOE_MX_E4M3, true>), g, b, 0, st, a);
+    else hipLaunchKernelGGL((mx_dequant_kernel<MOE_MX_E4M3, false>), g, b, 0, st, a);
     return check_launch("mx_dequant");
 }
 
