@@ -132,19 +132,17 @@ __device__ __forceinline__ double wave_sum_d(double v) {
     return v;
 }
 
-// A row is held by W waves (W = 1: four rows a workgroup; else one), NB octets
-// a lane, in registers from the load to the codes: one pass over memory. The
-// sum of squares is formed in fp64 (each square exact) and rounded once.
-//   * many rows: one wave a row, no barrier;
-//   * few rows, or rows above 4096 values: a workgroup of 256 to 1024 threads a
-//     row, so that a single token's row is in flight at once.
-template <int FMT, int NB, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? 1024 : 256) add_norm_kernel(AnArgs a) {
+// A workgroup of 64 to 1024 threads a row, NB octets a thread in registers from
+// the load to the codes: one pass over memory, and a single token's row is in
+// flight at once. The sum of squares is formed in fp64 (each square exact) and
+// rounded once. (A wave a row without a barrier, for many rows, was slower:
+// 4096 x 4096 30.5 us against 25.9, too little in flight at 8 octets a thread.)
+template <int FMT, int NB>
+__global__ void __launch_bounds__(1024) add_norm_kernel(AnArgs a) {
     __shared__ double s_part[16];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t t = WIDE ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + wave;
-    if (!WIDE && t >= a.T) return;
-    const int first = WIDE ? threadIdx.x : lane, step = WIDE ? blockDim.x : 64;
+    const int64_t t = blockIdx.x;
+    const int first = threadIdx.x, step = blockDim.x;
     const int row_octs = a.H >> 3;
     uint4 h[NB], r[NB];
 #pragma unroll
@@ -181,12 +179,10 @@ __global__ void __launch_bounds__(WIDE ? 1024 : 256) add_norm_kernel(AnArgs a) {
         for (int k = 0; k < 8; ++k) ss = __fma_rn((double)v[k], (double)v[k], ss);
     }
     ss = wave_sum_d(ss);
-    if constexpr (WIDE) {
-        if (lane == 0) s_part[wave] = ss;
-        __syncthreads();
-        ss = 0.0;
-        for (int w = 0; w < (int)(blockDim.x >> 6); ++w) ss += s_part[w];
-    }
+    if (lane == 0) s_part[wave] = ss;
+    __syncthreads();
+    ss = 0.0;
+    for (int w = 0; w < (int)(blockDim.x >> 6); ++w) ss += s_part[w];
     const float ms = __double2float_rn(__ddiv_rn(ss, (double)a.H));
     // sqrtf, not __fsqrt_rn: the latter is the bare v_sqrt_f32 here, which is off
     // by an ulp now and then
@@ -207,21 +203,12 @@ __global__ void __launch_bounds__(WIDE ? 1024 : 256) add_norm_kernel(AnArgs a) {
 
 template <int FMT>
 void launch_add_norm(const AnArgs& a, hipStream_t s) {
-    // One wave a row from 1024 rows on (four waves a CU); below, the row is
-    // split over a workgroup.
-    if (a.T >= 1024 && a.H <= 4096) {
-        const dim3 g((unsigned)((a.T + 3) / 4)), b(256);
-        if (a.H <= 1024) hipLaunchKernelGGL((add_norm_kernel<FMT, 2, false>), g, b, 0, s, a);
-        else if (a.H <= 2048) hipLaunchKernelGGL((add_norm_kernel<FMT, 4, false>), g, b, 0, s, a);
-        else hipLaunchKernelGGL((add_norm_kernel<FMT, 8, false>), g, b, 0, s, a);
-        return;
-    }
     const int octs = a.H >> 3;
     int threads = (octs + 63) / 64 * 64;
     if (threads > 1024) threads = 1024;
     const dim3 g((unsigned)a.T), b((unsigned)threads);
-    if (octs <= 1024) hipLaunchKernelGGL((add_norm_kernel<FMT, 1, true>), g, b, 0, s, a);
-    else hipLaunchKernelGGL((add_norm_kernel<FMT, 2, true>), g, b, 0, s, a);
+    if (octs <= 1024) hipLaunchKernelGGL((add_norm_kernel<FMT, 1>), g, b, 0, s, a);
+    else hipLaunchKernelGGL((add_norm_kernel<FMT, 2>), g, b, 0, s, a);
 }
 
 // Sizes, format, alignment and strides of an MX conversion between [T, H] bf16
