@@ -192,7 +192,7 @@ struct MgShape {
     // K of a stage: 256 where an operand is e2m1 (128 bytes of its rows), but for
     // the wider blocks with e4m3 tokens, of which LDS would hold too few stages
     // (2048 x 4096 x 4096 in 128-wide blocks: 48.3 us with 256, 41.2 with 128)
-    static constexpr int kElems = FA == MOE_MX_E2M1 || (FW == MOE_MX_E2M1 && MW * NW < 4) ? 256 : 128;
+    static constexpr int kElems = FA == MOE_MX_E2M1 || MW * NW < 4 ? 256 : 128;
     static constexpr int kSteps = kElems / 64;
     static constexpr int kABytes = FA == MOE_MX_E2M1 ? kElems / 2 : kElems;
     static constexpr int kWBytes = FW == MOE_MX_E2M1 ? kElems / 2 : kElems;
@@ -300,35 +300,91 @@ __device__ __forceinline__ MxFrag<FMT> mg_read(const uint8_t* rows, int row, int
     return f;
 }
 
-// The scales of blocks [b, b + 4) of a row in LDS, a byte each, zeros behind the
-// row's nb.
-template <int PIECES, bool ALIGNED>
-__device__ __forceinline__ uint32_t mg_scale_word(const uint8_t* row, int b, int nb) {
-    if constexpr (ALIGNED) {
-        const int piece = b & ~15, at = piece < nb - 16 ? piece : nb - 16;
-        const uint32_t v = *reinterpret_cast<const uint32_t*>(row + (PIECES == 2 ? b & 16 : 0) + (b < nb ? b - at : 0));
-        return b < nb ? v : 0u;
-    } else {
-        const uint4 v = *reinterpret_cast<const uint4*>(row + (b & 15) * 4);
-        return v.x | (v.y << 8) | (v.z << 16) | (v.w << 24);
-    }
-}
-
-// A stage's scales of a lane's row as one register: step s's in byte s, or with 2
-// steps in byte 2 s. b0: the stage's first block.
+// A stage's scales of a lane's row. read() takes what LDS holds and scales() makes
+// one register of it, step s's byte at s, or with 2 steps at 2 s, zeros behind
+// the row's nb blocks: apart, so that no instruction waits for the LDS between
+// the reads and the MFMAs that cover them. b0: the stage's first block.
 template <int STEPS, bool PAIR, int PIECES, bool ALIGNED>
-__device__ __forceinline__ uint32_t mg_scales(const uint8_t* row, int b0, int nb, int g) {
-    if constexpr (!PAIR) return mg_scale_word<PIECES, ALIGNED>(row, b0 + 4 * g, nb);        // blocks 4 g + step
-    const uint32_t v = mg_scale_word<PIECES, ALIGNED>(row, b0, nb);
-    if constexpr (STEPS == 2) return v >> (8 * g);                                  // blocks g, 2 + g
-    const uint32_t w = mg_scale_word<PIECES, ALIGNED>(row, b0 + 4, nb);                     // and 4 + g, 6 + g
-    return __builtin_amdgcn_perm(w, v, g ? 0x07050301u : 0x06040200u);
+struct MgScales {
+    static constexpr int kWords = PAIR && STEPS == 4 ? 2 : 1;       // of 4 blocks each
+    uint4 raw[kWords];                                              // aligned: x alone
+    __device__ __forceinline__ static int block(int b0, int i, int g) { return b0 + 4 * (PAIR ? i : g); }
+    __device__ __forceinline__ void read(const uint8_t* row, int b0, int nb, int g) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            const int b = block(b0, i, g);
+            if constexpr (ALIGNED) {
+                const int piece = b & ~15, at = piece < nb - 16 ? piece : nb - 16;
+                raw[i].x = *reinterpret_cast<const uint32_t*>(row + (PIECES == 2 ? b & 16 : 0) + (b < nb ? b - at : 0));
+            } else {
+                raw[i] = *reinterpret_cast<const uint4*>(row + (b & 15) * 4);
+            }
+        }
+    }
+    __device__ __forceinline__ uint32_t scales(int b0, int nb, int g) const {
+        uint32_t v[kWords];
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            if constexpr (ALIGNED) v[i] = block(b0, i, g) < nb ? raw[i].x : 0u;
+            else v[i] = raw[i].x | (raw[i].y << 8) | (raw[i].z << 16) | (raw[i].w << 24);
+        }
+        if constexpr (!PAIR) return v[0];                               // blocks 4 g + step
+        else if constexpr (STEPS == 2) return v[0] >> (8 * g);          // blocks g, 2 + g
+        else return __builtin_amdgcn_perm(v[1], v[0], g ? 0x07050301u : 0x06040200u);   // and 4 + g, 6 + g
+    }
+};
+
+// Epilogue of 32 tokens: a lane holds 4 consecutive columns of one token at a
+// time. The wave turns its NW tiles through its own part of the LDS (a token's
+// columns, padded by 16 bytes) and stores whole 16-byte pieces of the tokens'
+// rows. NT: outputs of 256-wide blocks are past what the L2 keeps for a reader,
+// non-temporal stores (4096 x 4096 x 4096 e2m1: 43.4 -> 42.6 us).
+template <int NW, bool F32>
+constexpr int out_row_bytes() { return 32 * NW * (F32 ? 4 : 2) + 16; }
+
+template <int NW, bool F32, bool NT>
+__device__ __forceinline__ void store_rows(const MgArgs& a, uint8_t* slab, const mx_f16v (&acc)[NW], int64_t t0, int64_t n0,
+                                           int lane) {
+    constexpr int kRow = out_row_bytes<NW, F32>(), kEs = F32 ? 4 : 2, kPiece = 16 / kEs, kPieces = 32 * NW / kPiece;
+    const int r = lane & 31, g = lane >> 5;
+    wave_lds_sync();
+#pragma unroll
+    for (int n = 0; n < NW; ++n)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int c = 32 * n + 8 * q + 4 * g;
+            const mx_f16v& v = acc[n];
+            if constexpr (F32)
+                *reinterpret_cast<floatx4*>(slab + r * kRow + c * 4) = floatx4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+            else
+                *reinterpret_cast<uint2*>(slab + r * kRow + c * 2) =
+                    make_uint2(bf16x2_pack(v[4 * q], v[4 * q + 1]), bf16x2_pack(v[4 * q + 2], v[4 * q + 3]));
+        }
+    wave_lds_sync();
+#pragma unroll
+    for (int j = 0; j < 32 * kPieces / 64; ++j) {
+        const int i = lane + 64 * j, tr = i / kPieces, c = (i % kPieces) * kPiece;
+        const int64_t t = t0 + tr, n = n0 + c;
+        if (t >= a.T || n >= a.N) continue;
+        const uint8_t* src = slab + tr * kRow + c * kEs;
+        uint8_t* dst = (uint8_t*)a.out + (t * a.out_stride + n) * kEs;
+        if (a.out_vec && n + kPiece <= a.N) {
+            const u32x4 v = *reinterpret_cast<const u32x4*>(src);
+            if constexpr (NT) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(dst));
+            else *reinterpret_cast<u32x4*>(dst) = v;
+        } else {
+            for (int e = 0; e < kPiece && n + e < a.N; ++e) {
+                if constexpr (F32) reinterpret_cast<float*>(dst)[e] = reinterpret_cast<const float*>(src)[e];
+                else reinterpret_cast<uint16_t*>(dst)[e] = reinterpret_cast<const uint16_t*>(src)[e];
+            }
+        }
+    }
 }
 
 template <int FA, int FW, int MW, int NW, bool ALIGNED, bool F32>
 __global__ void __launch_bounds__(256, (MgShape<FA, FW, MW, NW, ALIGNED>::kPerCu)) mx_gemm_tiled_kernel(MgArgs a) {
     using S = MgShape<FA, FW, MW, NW, ALIGNED>;
-    constexpr int kOutRow = 32 * NW * (F32 ? 4 : 2) + 16;       // one token's columns of a wave in the epilogue
+    constexpr int kOutRow = out_row_bytes<NW, F32>();
     constexpr int kLds = S::kLds > 4 * 32 * kOutRow ? S::kLds : 4 * 32 * kOutRow;
     constexpr bool kPair = FA == MOE_MX_E4M3;
     using Sf = typename S::Sf;
@@ -374,13 +430,21 @@ __global__ void __launch_bounds__(256, (MgShape<FA, FW, MW, NW, ALIGNED>::kPerCu
             else cw.issue(at + S::kW, s, q - S::kACopies, wave, w_row);
         }
     };
-    auto scales = [&](int s, uint32_t (&sa)[MW], uint32_t (&sw)[NW]) {
+    using Scales = MgScales<S::kSteps, kPair, S::kPieces, ALIGNED>;
+    Scales na[MW], nw[NW];      // the next stage's, as read
+    uint32_t sa[MW], sw[NW];
+    auto read_scales = [&](int s) {
         const uint8_t* at = lds + S::kSf + (s / S::kSpc & 1) * S::kChunk;
-        const int b0 = s * (S::kElems / 32);
 #pragma unroll
-        for (int m = 0; m < MW; ++m) sa[m] = mg_scales<S::kSteps, kPair, S::kPieces, ALIGNED>(at + Sf::kRow * (32 * (wm * MW + m) + r), b0, nb, g);
+        for (int m = 0; m < MW; ++m) na[m].read(at + Sf::kRow * (32 * (wm * MW + m) + r), s * (S::kElems / 32), nb, g);
 #pragma unroll
-        for (int n = 0; n < NW; ++n) sw[n] = mg_scales<S::kSteps, kPair, S::kPieces, ALIGNED>(at + Sf::kRow * (S::kBM + 32 * (wn * NW + n) + r), b0, nb, g);
+        for (int n = 0; n < NW; ++n) nw[n].read(at + Sf::kRow * (S::kBM + 32 * (wn * NW + n) + r), s * (S::kElems / 32), nb, g);
+    };
+    auto take_scales = [&](int s) {
+#pragma unroll
+        for (int m = 0; m < MW; ++m) sa[m] = na[m].scales(s * (S::kElems / 32), nb, g);
+#pragma unroll
+        for (int n = 0; n < NW; ++n) sw[n] = nw[n].scales(s * (S::kElems / 32), nb, g);
     };
     struct Operands {
         MxFrag<FA> a[MW];
@@ -401,7 +465,6 @@ __global__ void __launch_bounds__(256, (MgShape<FA, FW, MW, NW, ALIGNED>::kPerCu
         for (int n = 0; n < NW; ++n)
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[m][n][i] = 0.0f;
-    uint32_t sa[MW], sw[NW], sa1[MW], sw1[NW];
     // one MFMA row of a step; the scales' byte SEL
     auto mfma = [&](const Operands& o, int m, auto sel) {
 #pragma unroll
@@ -421,8 +484,9 @@ __global__ void __launch_bounds__(256, (MgShape<FA, FW, MW, NW, ALIGNED>::kPerCu
     Operands o0, o1;
     __builtin_amdgcn_s_waitcnt(vmcnt_at_most((S::kRing - 1) * kAll));
     __syncthreads();
-    scales(0, sa, sw);
+    read_scales(0);
     read(0, 0, o0);
+    take_scales(0);
     for (int s = 0; s < stages; ++s) {
         read(s, 1, o1);
         mfmas(o0, std::integral_constant<int, 0>());
@@ -435,7 +499,7 @@ __global__ void __launch_bounds__(256, (MgShape<FA, FW, MW, NW, ALIGNED>::kPerCu
         __builtin_amdgcn_s_waitcnt(vmcnt_at_most((S::kRing - 2) * kAll) & lgkmcnt_zero());
         asm volatile("s_barrier" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
-        scales(s + 1, sa1, sw1);
+        read_scales(s + 1);
         read(s + 1, 0, o0);
 #pragma unroll
         for (int m = 0; m < MW; ++m) {
@@ -443,58 +507,16 @@ __global__ void __launch_bounds__(256, (MgShape<FA, FW, MW, NW, ALIGNED>::kPerCu
             mfma(o1, m, std::integral_constant<int, S::kSteps == 4 ? 3 : 2>());
             __builtin_amdgcn_sched_barrier(0);
         }
-#pragma unroll
-        for (int m = 0; m < MW; ++m) sa[m] = sa1[m];
-#pragma unroll
-        for (int n = 0; n < NW; ++n) sw[n] = sw1[n];
+        take_scales(s + 1);
     }
     // the copies of the stages behind the last still write (zeros) to the LDS
     __builtin_amdgcn_s_waitcnt(vmcnt_at_most(0) & lgkmcnt_zero());
     __syncthreads();
 
-    // Epilogue: a lane holds 4 consecutive columns of one token at a time. Each
-    // wave turns 32 tokens of its columns through its own part of the LDS and
-    // stores whole 16-byte pieces of a token's row.
-    constexpr int kEs = F32 ? 4 : 2, kPiece = 16 / kEs, kPieces = 32 * NW / kPiece;
     uint8_t* slab = lds + wave * 32 * kOutRow;
 #pragma unroll
-    for (int m = 0; m < MW; ++m) {
-        wave_lds_sync();
-#pragma unroll
-        for (int n = 0; n < NW; ++n)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int c = 32 * n + 8 * q + 4 * g;
-                const mx_f16v& v = acc[m][n];
-                if constexpr (F32)
-                    *reinterpret_cast<floatx4*>(slab + r * kOutRow + c * 4) =
-                        floatx4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-                else
-                    *reinterpret_cast<uint2*>(slab + r * kOutRow + c * 2) =
-                        make_uint2(bf16x2_pack(v[4 * q], v[4 * q + 1]), bf16x2_pack(v[4 * q + 2], v[4 * q + 3]));
-            }
-        wave_lds_sync();
-#pragma unroll
-        for (int j = 0; j < 32 * kPieces / 64; ++j) {
-            const int i = lane + 64 * j, tr = i / kPieces, c = (i % kPieces) * kPiece;
-            const int64_t t = m0 + 32 * (wm * MW + m) + tr, n = n0 + 32 * NW * wn + c;
-            if (t >= a.T || n >= a.N) continue;
-            const uint8_t* src = slab + tr * kOutRow + c * kEs;
-            uint8_t* dst = (uint8_t*)a.out + (t * a.out_stride + n) * kEs;
-            if (a.out_vec && n + kPiece <= a.N) {
-                // outputs of 256-wide blocks are past what the L2 keeps for a reader:
-                // non-temporal stores (4096 x 4096 x 4096 e2m1: 43.4 -> 42.6 us)
-                const u32x4 v = *reinterpret_cast<const u32x4*>(src);
-                if constexpr (MW * NW >= 16) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(dst));
-                else *reinterpret_cast<u32x4*>(dst) = v;
-            } else {
-                for (int e = 0; e < kPiece && n + e < a.N; ++e) {
-                    if constexpr (F32) reinterpret_cast<float*>(dst)[e] = reinterpret_cast<const float*>(src)[e];
-                    else reinterpret_cast<uint16_t*>(dst)[e] = reinterpret_cast<const uint16_t*>(src)[e];
-                }
-            }
-        }
-    }
+    for (int m = 0; m < MW; ++m)
+        store_rows<NW, F32, (MW * NW >= 16)>(a, slab, acc[m], m0 + 32 * (wm * MW + m), n0 + 32 * NW * wn, lane);
 }
 
 template <int FA, int FW, int MW, int NW, bool ALIGNED>

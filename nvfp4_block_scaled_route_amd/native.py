@@ -363,7 +363,7 @@ def _where(call, t, stream) -> tuple[int, int]:
     first tensor is a host tensor, which the checks refuse."""
     if t.get_device() < 0:
         return -2, 0
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()
     if stream is None:
         return dev, torch._C._cuda_getCurrentRawStream(dev)
     if hasattr(stream, "cuda_stream"):
