@@ -4,7 +4,8 @@ The step order is the model page's "_prepared_nvfp4_forward" and the runner
 page's "MuseSparkTrtLlmNvFp4Experts.apply_routed" / "MusePostExpertFinalize":
 route, quantize the expert input, experts up to the GEMM2 rows, finalize. This
 module only allocates device buffers (torch) and calls the library; all
-arithmetic runs in the HIP kernels.
+arithmetic runs in the HIP kernels. MxLinear is a dense projection in front of
+or behind that path.
 
 Expert TP on one GPU (the expert_tp page): the tp slices of the converted
 weights are byte views (``slice_weights``); each slice's experts write their
@@ -56,6 +57,44 @@ def slice_weights(full: N.Weights, r: int, tp: int, H: int, I: int) -> N.Weights
         w13_offset=full.w13_offset + p13 * full.w13_pair_stride,
         w13_sf_offset=full.w13_sf_offset + p13 * full.w13_sf_pair_stride,
         w2_offset=full.w2_offset + t2 * 1024, w2_sf_offset=full.w2_sf_offset + t2 * 128)
+
+
+class MxLinear:
+    """A dense projection around the experts (the model page, "MuseSpark1xMoE":
+    the pooler and unpooler) in MX formats: out = x times weight transposed, the
+    weight [N, K] (bf16) quantized once, x per call. Holds the buffers of calls
+    with up to max_tokens rows, so calls can be captured, and calls that share
+    one MxLinear must not overlap (as calls that share one Buffers)."""
+
+    def __init__(self, weight_bf16, max_tokens: int, w_fmt: int = N.MOE_MX_E2M1, a_fmt: int = N.MOE_MX_E4M3, stream=None):
+        n, k = weight_bf16.shape
+        self.N, self.K, self.max_tokens, self.w_fmt, self.a_fmt = n, k, max_tokens, w_fmt, a_fmt
+        self.w_codes, self.w_sf = self._buffers(n, w_fmt, weight_bf16.device)
+        self.a_codes, self.a_sf = self._buffers(max_tokens, a_fmt, weight_bf16.device)
+        N.mx_quant(weight_bf16, w_fmt, self.w_codes, self.w_sf, stream)
+
+    def _buffers(self, rows, fmt, device):
+        width = self.K // 2 if fmt == N.MOE_MX_E2M1 else self.K
+        return (torch.empty((rows, width), dtype=torch.uint8, device=device),
+                torch.empty((rows, self.K // 32), dtype=torch.uint8, device=device))
+
+    def _rows(self, x):
+        if x.shape[0] > self.max_tokens:
+            raise ValueError(f"{x.shape[0]} tokens, more than the {self.max_tokens} this projection was made for")
+        return self.a_codes[:x.shape[0]], self.a_sf[:x.shape[0]]
+
+    def __call__(self, x, out, stream=None) -> None:
+        """out [T, N] = x [T, K] times the weight transposed; bf16 (out also fp32
+        where both formats are e2m1)."""
+        codes, sf = self._rows(x)
+        N.mx_quant(x, self.a_fmt, codes, sf, stream)
+        N.mx_gemm(codes, sf, self.a_fmt, self.w_codes, self.w_sf, self.w_fmt, out, stream)
+
+    def after_norm(self, x, residual, norm_weight, gain_center: float, eps: float, sum_out, out, stream=None) -> None:
+        """The same on the RMSNorm of sum_out = x + residual (mx_add_norm_quant)."""
+        codes, sf = self._rows(x)
+        N.mx_add_norm_quant(x, residual, norm_weight, gain_center, eps, self.a_fmt, sum_out, codes, sf, stream)
+        N.mx_gemm(codes, sf, self.a_fmt, self.w_codes, self.w_sf, self.w_fmt, out, stream)
 
 
 @dataclass

@@ -338,8 +338,8 @@ def _rows(call, name, t, dtypes, shape, dev) -> int:
     device `dev`, with rows of consecutive elements."""
     if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.get_device() == dev:
         if shape[0] <= 1:
-            if shape[1] <= 1 or t.stride(1) == 1:
-                return (shape[1] + 15) // 16 * 16       # one row: any stride will do
+            if shape[0] == 0 or shape[1] <= 1 or t.stride(1) == 1:
+                return (shape[1] + 15) // 16 * 16       # one row or none: any stride will do
         else:
             s = t.stride()
             if s[1] == 1 or shape[1] <= 1:
