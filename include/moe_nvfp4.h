@@ -555,7 +555,7 @@ int mx_add_norm_quant(const uint16_t* x, int64_t x_row_stride, const uint16_t* r
  * products is exact to fp32; where an operand is e4m3 the matrix cores cut each
  * product to 13 bits below the exponent of the largest of its 8, about 1.5e-5 of
  * the result. A NaN
- * scale makes the row or column NaN. K % 32 == 0, K <= MOE_MAX_MX_K; any T and
+ * scale or e4m3 NaN code makes the row or column NaN. K % 32 == 0, K <= MOE_MAX_MX_K; any T and
  * N. One launch on `stream`, no workspace. */
 int mx_gemm(const uint8_t* a_codes, const uint8_t* a_sf, int a_fmt, const uint8_t* w_codes, const uint8_t* w_sf,
             int w_fmt, int T, int N, int K, void* out, int64_t out_row_stride, int out_dtype, void* stream);
@@ -572,7 +572,8 @@ int mx_gemm(const uint8_t* a_codes, const uint8_t* a_sf, int a_fmt, const uint8_
  * are written; rows from total_rows on are left as they were. Every sum has a
  * fixed order: results do not change from call to call. Row strides count
  * elements and are >= H and % 8 == 0 (moe_dispatch: bytes, >= row_bytes, % 16 == 0).
- * dtype: MOE_BF16 or MOE_F32, of rows and token rows alike. One launch each.
+ * dtype: MOE_BF16 or MOE_F32, of rows and token rows alike. One launch each; with
+ * T or H (row_bytes) zero nothing is launched or written.
  *
  * moe_dispatch: rows[p(t,k)] = x[t], rows of any type as bytes (quantized codes
  * and scales too); row_bytes % 16 == 0, at most 4 * MOE_MAX_HIDDEN. */

@@ -25,6 +25,8 @@ int moe_route_check(int T, int E, int K, int tile_m, int local_expert_offset, in
 // experts (g1_scale_c checked when need_scale_c): shared by the expert calls
 // and moe_validate_weights
 int check_weights(const moe_nvfp4_weights* w, int H, int I, bool need_scale_c, const char* name);
+// whether a launch of so many workgroups fits (its threads are counted in 32 bits)
+inline bool launch_fits(int64_t groups, int threads) { return groups <= 0xFFFFFFFFLL / threads && groups <= 0x7FFFFFFF; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 moe_meta_layout meta_layout(int T, int K, int E_local, int tile_m);
 // int32 words between the sync counters of consecutive 16-row tiles in the

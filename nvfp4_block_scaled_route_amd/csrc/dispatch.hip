@@ -249,7 +249,7 @@ static int launch_combine(const void* rows, int64_t rows_stride, int dtype, cons
     const int threads = (int64_t)T * ((a.units + 255) / 256) >= 1024 ? 256 : 64;
     a.col_groups = (a.units + threads - 1) / threads;
     const int64_t grid = (int64_t)T * a.col_groups;
-    if (grid > 0x7FFFFFFF) return fail(MOE_EUNSUPPORTED, "%s: too large", name);
+    if (!launch_fits(grid, threads)) return fail(MOE_EUNSUPPORTED, "%s: too large", name);
     const dim3 g((unsigned)grid), b((unsigned)threads);
     if (dtype == MOE_F32) hipLaunchKernelGGL(combine_kernel<true>, g, b, 0, (hipStream_t)stream, a);
     else hipLaunchKernelGGL(combine_kernel<false>, g, b, 0, (hipStream_t)stream, a);
@@ -301,7 +301,7 @@ extern "C" int moe_dispatch(const void* x, int64_t x_row_stride_bytes, int64_t r
     const bool split = T < kRouteSplitTokens;
     a.col_groups = (a.units + 255) / 256;
     const int64_t work = (int64_t)T * (split ? K : 1) * a.col_groups, pad = (rows_max + kPadRows - 1) / kPadRows;
-    if (work + pad > 0x7FFFFFFF) return fail(MOE_EUNSUPPORTED, "%s: too large", name);
+    if (!launch_fits(work + pad, 256)) return fail(MOE_EUNSUPPORTED, "%s: too large", name);
     a.work_groups = (int)work;
     const dim3 g((unsigned)(work + pad)), b(256);
     if (split) hipLaunchKernelGGL(dispatch_kernel<true>, g, b, 0, (hipStream_t)stream, a);
@@ -361,7 +361,7 @@ extern "C" int moe_combine_bwd(const void* d_out, int64_t d_out_row_stride, cons
     a.rows = (uint8_t*)d_rows; a.rows_stride = d_rows_stride * es; a.d_weights = d_weights;
     const bool split = T < kRouteSplitTokens;
     const int64_t work = (int64_t)T * (split ? K : 1), pad = (rows_max + kPadRows - 1) / kPadRows;
-    if (work + pad > 0x7FFFFFFF) return fail(MOE_EUNSUPPORTED, "%s: too large", name);
+    if (!launch_fits(work + pad, a.units <= 256 ? 256 : a.units <= 512 ? 512 : 1024)) return fail(MOE_EUNSUPPORTED, "%s: too large", name);
     a.work_groups = (int)work;
     if (dtype == MOE_F32) launch_combine_bwd<true>(a, (unsigned)(work + pad), split, (hipStream_t)stream);
     else launch_combine_bwd<false>(a, (unsigned)(work + pad), split, (hipStream_t)stream);

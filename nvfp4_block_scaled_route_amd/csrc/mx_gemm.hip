@@ -538,13 +538,14 @@ int launch_mx_gemm(const MgArgs& a, hipStream_t s) {
     // K = N = 4096, e4m3 x e2m1: 32 tokens 9.7 us by columns, 10.6 in 64-wide
     // blocks; 64 tokens 15.6 and 11.0
     if (a.T <= 32) {
-        const dim3 g((unsigned)((a.N + 15) / 16)), b(64 * kSkWaves);
+        const dim3 g((unsigned)(((int64_t)a.N + 15) / 16)), b(64 * kSkWaves);
+        if (!launch_fits(g.x, b.x)) return fail(MOE_EUNSUPPORTED, "%s: too many columns", name);
         if (a.T <= 16) hipLaunchKernelGGL((mx_gemm_skinny_kernel<FA, FW, 1, ALIGNED>), g, b, 0, s, a);
         else hipLaunchKernelGGL((mx_gemm_skinny_kernel<FA, FW, 2, ALIGNED>), g, b, 0, s, a);
         return check_launch(name);
     }
-    const auto tiles = [&](int bm, int bn) { return (int64_t)((a.T + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
-    if (tiles(64, 64) > 0x7FFFFFFF) return fail(MOE_EUNSUPPORTED, "%s: too many output tiles", name);
+    const auto tiles = [&](int64_t bm, int64_t bn) { return (a.T + bm - 1) / bm * ((a.N + bn - 1) / bn); };
+    if (!launch_fits(tiles(64, 64), 256)) return fail(MOE_EUNSUPPORTED, "%s: too many output tiles", name);
     // The widest block that fills the chip: wide blocks read less per product,
     // but a CU without one idles. us with K = 4096 (64 x 64, 64 x 128, 128 x 128,
     // 256 x 256):

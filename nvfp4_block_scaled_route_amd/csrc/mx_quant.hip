@@ -224,7 +224,7 @@ static int mx_check(const void* x, int64_t x_row_stride, int T, int H, int fmt, 
         return fail(MOE_EINVAL, "%s: pointers must be 16-byte aligned", name);
     if (x_row_stride < H || x_row_stride % 8)
         return fail(MOE_EINVAL, "%s: row stride %lld must be >= H and a multiple of 8", name, (long long)x_row_stride);
-    if (((int64_t)T * (H / 8) + kMqThreads - 1) / kMqThreads > 0x7FFFFFFF)
+    if (!launch_fits(((int64_t)T * (H / 8) + kMqThreads - 1) / kMqThreads, kMqThreads))
         return fail(MOE_EUNSUPPORTED, "%s: too large", name);
     return MOE_OK;
 }
@@ -268,6 +268,7 @@ extern "C" int mx_add_norm_quant(const uint16_t* x, int64_t x_row_stride, const 
     const int rc = mx_check(x, x_row_stride, T, H, fmt, codes, sf, name);
     if (rc != MOE_OK) return rc;
     if (H > MOE_MAX_HIDDEN) return fail(MOE_EUNSUPPORTED, "%s: H=%d above %d", name, H, MOE_MAX_HIDDEN);
+    if (!launch_fits(T, 1024)) return fail(MOE_EUNSUPPORTED, "%s: too many rows", name);
     if (!(eps > 0.0f) || eps > 1.0f || !(gain_center == gain_center))
         return fail(MOE_EINVAL, "%s: eps must be in (0, 1] and the gain centre a number", name);
     if (T == 0 || H == 0) return MOE_OK;

@@ -86,6 +86,15 @@ def test_library_refuses(call, want, kw):
     assert N.lib().moe_last_error()
 
 
+@pytest.mark.parametrize("call,kw", [
+    (quant, dict(T=1 << 30, H=64)), (dequant, dict(T=1 << 30, H=64)), (norm, dict(T=1 << 23)), (gemm, dict(T=1, Nn=2 ** 31 - 1, ld=2 ** 31 - 1)),
+    (gemm, dict(T=1 << 20, Nn=1 << 20, ld=1 << 20)), (dispatch, dict(T=1 << 24, K=8)), (dispatch_bwd, dict(T=1 << 27)),
+    (combine, dict(T=1 << 25)), (combine_bwd, dict(T=1 << 26, K=1)),
+    (combine_bwd, dict(T=1 << 22, K=1, H=16384, ldo=16384, ldr=16384, ldd=16384))])
+def test_library_refuses_more_threads_than_a_launch_counts(call, kw):
+    assert call(**kw) == N.MOE_EUNSUPPORTED, N.lib().moe_last_error()
+
+
 @pytest.mark.parametrize("call,kw", [(quant, dict(T=0, x=0)), (quant, dict(H=0, x=0, ld=0)), (dequant, dict(T=0)),
                                      (norm, dict(T=0, x=0)), (gemm, dict(T=0, a=0)), (gemm, dict(Nn=0, w=0)),
                                      (dispatch, dict(T=0, x=0)), (dispatch, dict(nb=0)), (dispatch_bwd, dict(T=0)),
