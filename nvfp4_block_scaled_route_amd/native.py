@@ -273,8 +273,7 @@ def moe_experts_finalize(a_codes, a_sf, meta, weights: Weights, T, K, E_local, H
                                       rows.stride(-2), n_partials, partial_stride, _ptr(topk_weights),
                                       _ptr(norm_weight), float(gain_center), float(eps),
                                       int(weight_before_norm), _ptr(out), _stream(stream)),
-           "moe_experts_finalize", "mx_quant", "mx_dequant", "mx_add_norm_quant", "mx_gemm",
-           "moe_dispatch", "moe_dispatch_bwd", "moe_combine", "moe_combine_bwd")
+           "moe_experts_finalize")
 
 
 def moe_experts_fwd_noalloc(a_codes, a_sf, meta, weights: Weights, T, K, E_local, H, I, tile_m,
