@@ -9,7 +9,9 @@
  *   [model]          vllm.models.muse_spark.nvidia.model
  * A layer runs, on one stream, in this order:
  *   moe_route -> nvfp4_quant -> moe_experts_fwd -> moe_finalize
- * (moe_route_quant is the first two in one launch)
+ * (moe_route_quant is the first two in one launch); beside it stand dense
+ * products in MX formats (mx_*) and the sort of tokens by expert and back
+ * (moe_dispatch, moe_combine), with the gradients
  * (the model page, "_prepared_nvfp4_forward", prepares the quantized input and
  * the routing; the runner page, "MuseSparkTrtLlmNvFp4Experts.apply_routed", runs
  * the experts up to the GEMM2 rows and hands them to "MusePostExpertFinalize").
