@@ -137,6 +137,13 @@ __device__ __forceinline__ uint32_t nvfp4_codes8(const float* v, const BlockScal
     return bs.r == 0.0f ? 0u : w;
 }
 
+// ------------------------------------------------------------------ streamed rows
+// A non-temporal 16-byte store, for outputs far larger than an L2.
+typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ void store_stream16(void* p, uint4 v) {
+    __builtin_nontemporal_store(u32x4_t{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4_t*>(p));
+}
+
 // ------------------------------------------------------------------ sigmoid
 // s(l) = 1 / (1 + exp(-l)). exp by Cody and Waite's range reduction
 // x = n ln2 + r, with ln2 split so that n * ln2_hi is exact, and the degree-7

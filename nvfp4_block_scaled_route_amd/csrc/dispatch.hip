@@ -19,8 +19,10 @@ namespace moe {
 
 constexpr int kPadRows = 16;        // permuted rows a padding workgroup looks at (tiles are multiples of 16)
 constexpr int kSortBatch = 8;       // routes whose loads issue together
-// Below so many tokens a workgroup takes one route instead of one token: with
-// few tokens there are too few workgroups to have the rows in flight at once.
+// moe_combine_bwd: below so many tokens a workgroup takes one route instead of
+// one token, for more rows in flight (8 tokens 4.7 us against 9.2, 256 tokens
+// 12.7 against 13.6, 512 tokens 20.7 against 18.9). moe_dispatch gains nothing
+// by it (8 tokens 4.8 and 4.7 us, 256 tokens 9.8 and 7.0).
 constexpr int kRouteSplitTokens = 512;
 
 struct SortArgs {
@@ -42,10 +44,12 @@ struct SortArgs {
     int col_groups;                 // workgroups a token or route is split into
 };
 
-typedef unsigned int sort_u32x4 __attribute__((ext_vector_type(4)));
-
 __device__ __forceinline__ uint4 load16(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
-__device__ __forceinline__ void store16(uint8_t* p, uint4 v) { *reinterpret_cast<uint4*>(p) = v; }
+// Non-temporal: the rows written are far more than an L2 holds, and without it
+// they displace the rows read (4096 tokens x 4096 bf16, top-8 of 128 experts:
+// moe_dispatch 107.8 -> 69.8 us, moe_combine_bwd 176.1 -> 129.2, moe_combine
+// 64.1 -> 57.3; from 1 to 512 tokens the same or up to 30% faster).
+__device__ __forceinline__ void store16(uint8_t* p, uint4 v) { store_stream16(p, v); }
 
 // A route's permuted row, or -1 (absent, or outside the rows).
 __device__ __forceinline__ int64_t route_row(const int32_t* exp2perm, int64_t route, int64_t R) {
@@ -72,16 +76,14 @@ __device__ __forceinline__ void zero_padding(const SortArgs& a, int64_t group) {
 }
 
 // moe_dispatch: a workgroup copies 256 units of one token's row to the rows of
-// all its routes, or (kSplit) of one route.
-template <bool kSplit>
+// all its routes.
 __global__ void __launch_bounds__(256) dispatch_kernel(SortArgs a) {
     if ((int)blockIdx.x >= a.work_groups) return zero_padding(a, (int)blockIdx.x - a.work_groups);
-    const int item = blockIdx.x / a.col_groups, c = blockIdx.x - item * a.col_groups;
-    const int t = kSplit ? item / a.K : item, k0 = kSplit ? item - t * a.K : 0, k1 = kSplit ? k0 + 1 : a.K;
+    const int t = blockIdx.x / a.col_groups, c = blockIdx.x - t * a.col_groups;
     const int u = c * (int)blockDim.x + threadIdx.x;
     if (u >= a.units) return;
     const uint4 v = load16(a.tok + t * a.tok_stride + (int64_t)u * 16);
-    for (int k = k0; k < k1; ++k) {
+    for (int k = 0; k < a.K; ++k) {
         const int64_t p = route_row(a.exp2perm, (int64_t)t * a.K + k, a.R);
         if (p >= 0) store16(a.rows + p * a.rows_stride + (int64_t)u * 16, v);
     }
@@ -245,8 +247,9 @@ static int launch_combine(const void* rows, int64_t rows_stride, int dtype, cons
     a.rows_in = (const uint8_t*)rows; a.rows_in_stride = rows_stride * es;
     a.exp2perm = exp2perm; a.weights = weights; a.T = T; a.K = K; a.R = rows_max;
     a.units = H * es / 16; a.rows = (uint8_t*)out; a.rows_stride = out_row_stride * es;
-    // 64-thread workgroups while there are fewer than four 256-thread ones a CU
-    const int threads = (int64_t)T * ((a.units + 255) / 256) >= 1024 ? 256 : 64;
+    // 64-thread workgroups while there is less than one of 256 threads a CU (8192
+    // bytes a token: 64 tokens 4.2 us against 4.4, 128 tokens 5.4 against 4.9)
+    const int threads = (int64_t)T * ((a.units + 255) / 256) >= 256 ? 256 : 64;
     a.col_groups = (a.units + threads - 1) / threads;
     const int64_t grid = (int64_t)T * a.col_groups;
     if (!launch_fits(grid, threads)) return fail(MOE_EUNSUPPORTED, "%s: too large", name);
@@ -298,14 +301,12 @@ extern "C" int moe_dispatch(const void* x, int64_t x_row_stride_bytes, int64_t r
     a.tok = (const uint8_t*)x; a.tok_stride = x_row_stride_bytes; a.exp2perm = exp2perm; a.perm2tok = perm2tok;
     a.total_rows = total_rows; a.T = T; a.K = K; a.R = rows_max; a.units = (int)(row_bytes / 16);
     a.rows = (uint8_t*)rows; a.rows_stride = rows_stride_bytes;
-    const bool split = T < kRouteSplitTokens;
     a.col_groups = (a.units + 255) / 256;
-    const int64_t work = (int64_t)T * (split ? K : 1) * a.col_groups, pad = (rows_max + kPadRows - 1) / kPadRows;
+    const int64_t work = (int64_t)T * a.col_groups, pad = (rows_max + kPadRows - 1) / kPadRows;
     if (!launch_fits(work + pad, 256)) return fail(MOE_EUNSUPPORTED, "%s: too large", name);
     a.work_groups = (int)work;
     const dim3 g((unsigned)(work + pad)), b(256);
-    if (split) hipLaunchKernelGGL(dispatch_kernel<true>, g, b, 0, (hipStream_t)stream, a);
-    else hipLaunchKernelGGL(dispatch_kernel<false>, g, b, 0, (hipStream_t)stream, a);
+    hipLaunchKernelGGL(dispatch_kernel, g, b, 0, (hipStream_t)stream, a);
     return check_launch(name);
 }
 

@@ -240,6 +240,18 @@ def test_gemm_special_scales(T):
             assert (np.abs(got - ref) <= tol).all()
 
 
+@pytest.mark.parametrize("T", [5, 40, 200])
+def test_gemm_e4m3_nan_codes(T):
+    """An e4m3 NaN code makes its token's row NaN and nothing else, in K's last block too."""
+    rng = np.random.default_rng(T)
+    for K in (96, 640):
+        (ac, asf), (wc, wsf) = _values(rng, T, K, "e4m3"), _values(rng, 70, K, "e4m3")
+        ac[2, K - 1], ac[4, 0], wc[69, 33] = 0x7F, 0xFF, 0x7F
+        nan = np.zeros((T, 70), bool)
+        nan[2], nan[4], nan[:, 69] = True, True, True
+        assert np.array_equal(np.isnan(_gemm(ac, asf, "e4m3", wc, wsf, "e4m3")), nan)
+
+
 def test_gemm_e2m1_products_are_exact():
     """Small whole numbers: every partial sum is exact, so the fp32 output is."""
     rng = np.random.default_rng(0)
