@@ -19,11 +19,13 @@ namespace moe {
 
 constexpr int kPadRows = 16;        // permuted rows a padding workgroup looks at (tiles are multiples of 16)
 constexpr int kSortBatch = 8;       // routes whose loads issue together
-// moe_combine_bwd: below so many tokens a workgroup takes one route instead of
-// one token, for more rows in flight (8 tokens 4.7 us against 9.2, 256 tokens
-// 12.7 against 13.6, 512 tokens 20.7 against 18.9). moe_dispatch gains nothing
-// by it (8 tokens 4.8 and 4.7 us, 256 tokens 9.8 and 7.0).
-constexpr int kRouteSplitTokens = 512;
+// moe_combine_bwd: below so many 16-byte units of token rows (1 MiB) a workgroup
+// takes one route instead of one token, for more rows in flight. Top-8, split
+// and not: rows of 8 KiB, 8 tokens 4.5 and 6.6 us, 64 5.6 and 7.1, 128 7.8 and
+// 7.8, 256 12.0 and 10.5; of 2 KiB, 256 tokens 5.2 and 6.1, 512 7.7 and 7.7;
+// of 16 KiB, 64 tokens 10.3 and 10.8, 128 12.8 and 11.9. moe_dispatch gains
+// nothing by it (8 tokens 4.8 and 4.7 us).
+constexpr int64_t kRouteSplitUnits = 65536;
 
 struct SortArgs {
     const uint8_t* tok;             // token rows: x, or d_out
@@ -47,8 +49,8 @@ struct SortArgs {
 __device__ __forceinline__ uint4 load16(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
 // Non-temporal: the rows written are far more than an L2 holds, and without it
 // they displace the rows read (4096 tokens x 4096 bf16, top-8 of 128 experts:
-// moe_dispatch 107.8 -> 69.8 us, moe_combine_bwd 176.1 -> 129.2, moe_combine
-// 64.1 -> 57.3; from 1 to 512 tokens the same or up to 30% faster).
+// moe_dispatch 107.8 -> 65.4 us, moe_combine_bwd 176.1 -> 129.2, moe_combine
+// 64.1 -> 57.3; from 1 to 512 tokens the same or up to 30% less).
 __device__ __forceinline__ void store16(uint8_t* p, uint4 v) { store_stream16(p, v); }
 
 // A route's permuted row, or -1 (absent, or outside the rows).
@@ -151,7 +153,8 @@ __global__ void __launch_bounds__(256) combine_kernel(SortArgs a) {
 
 // moe_combine_bwd: a workgroup holds one token's d_out row in registers (NU
 // units a thread) for all its routes, or (kSplit) for one; batches of B routes
-// whose row loads issue together. The weight's gradient is a sum over the row:
+// whose row loads issue together (4096 tokens, top-8, rows of 8 KiB: NU = 1 and
+// B = 8 121.4 us, 2 and 4 129.0, 2 and 8 122.6; 512 tokens 15.7, 16.0, 16.2). The weight's gradient is a sum over the row:
 // per thread in fp32, then over the wave, then over the waves in order.
 template <bool kF32, int NU, int B, bool kSplit>
 __global__ void __launch_bounds__(1024) combine_bwd_kernel(SortArgs a) {
@@ -259,21 +262,21 @@ static int launch_combine(const void* rows, int64_t rows_stride, int dtype, cons
     return check_launch(name);
 }
 
+// A thread a unit up to 1024 threads, then 2 or 4 units a thread.
+static int bwd_threads(int units) { return units < 1024 ? (units + 63) / 64 * 64 : 1024; }
+
 template <bool kF32>
 void launch_combine_bwd(const SortArgs& a, unsigned grid, bool split, hipStream_t s) {
-    // units a thread: 1 up to 256 units (256 threads), then 2 up to 512, then
-    // 1024 threads with 4 (16384 fp32 values)
-    const dim3 g(grid);
-    if (a.units <= 256) {
-        const dim3 b((unsigned)((a.units + 63) / 64 * 64));
+    const dim3 g(grid), b((unsigned)bwd_threads(a.units));
+    if (a.units <= 1024) {
         if (split) hipLaunchKernelGGL((combine_bwd_kernel<kF32, 1, 1, true>), g, b, 0, s, a);
         else hipLaunchKernelGGL((combine_bwd_kernel<kF32, 1, 8, false>), g, b, 0, s, a);
-    } else if (a.units <= 512) {
-        if (split) hipLaunchKernelGGL((combine_bwd_kernel<kF32, 1, 1, true>), g, dim3(512), 0, s, a);
-        else hipLaunchKernelGGL((combine_bwd_kernel<kF32, 2, 4, false>), g, dim3(256), 0, s, a);
+    } else if (a.units <= 2048) {
+        if (split) hipLaunchKernelGGL((combine_bwd_kernel<kF32, 2, 1, true>), g, b, 0, s, a);
+        else hipLaunchKernelGGL((combine_bwd_kernel<kF32, 2, 4, false>), g, b, 0, s, a);
     } else {
-        if (split) hipLaunchKernelGGL((combine_bwd_kernel<kF32, 4, 1, true>), g, dim3(1024), 0, s, a);
-        else hipLaunchKernelGGL((combine_bwd_kernel<kF32, 4, 2, false>), g, dim3(1024), 0, s, a);
+        if (split) hipLaunchKernelGGL((combine_bwd_kernel<kF32, 4, 1, true>), g, b, 0, s, a);
+        else hipLaunchKernelGGL((combine_bwd_kernel<kF32, 4, 2, false>), g, b, 0, s, a);
     }
 }
 
@@ -360,9 +363,9 @@ extern "C" int moe_combine_bwd(const void* d_out, int64_t d_out_row_stride, cons
     a.exp2perm = exp2perm; a.perm2tok = perm2tok; a.total_rows = total_rows; a.weights = topk_weights;
     a.T = T; a.K = K; a.R = rows_max; a.units = H * es / 16;
     a.rows = (uint8_t*)d_rows; a.rows_stride = d_rows_stride * es; a.d_weights = d_weights;
-    const bool split = T < kRouteSplitTokens;
+    const bool split = (int64_t)T * a.units < kRouteSplitUnits;
     const int64_t work = (int64_t)T * (split ? K : 1), pad = (rows_max + kPadRows - 1) / kPadRows;
-    if (!launch_fits(work + pad, a.units <= 256 ? 256 : a.units <= 512 ? 512 : 1024)) return fail(MOE_EUNSUPPORTED, "%s: too large", name);
+    if (!launch_fits(work + pad, bwd_threads(a.units))) return fail(MOE_EUNSUPPORTED, "%s: too large", name);
     a.work_groups = (int)work;
     if (dtype == MOE_F32) launch_combine_bwd<true>(a, (unsigned)(work + pad), split, (hipStream_t)stream);
     else launch_combine_bwd<false>(a, (unsigned)(work + pad), split, (hipStream_t)stream);
