@@ -13,6 +13,7 @@ K-partial GEMM2 rows into ``rows[r]`` and the finalize sums them before the norm
 """
 from __future__ import annotations
 
+import contextlib
 from dataclasses import dataclass
 
 import torch
@@ -64,13 +65,20 @@ class MxLinear:
     the pooler and unpooler) in MX formats: out = x times weight transposed, the
     weight [N, K] (bf16) quantized once, x per call. Holds the buffers of calls
     with up to max_tokens rows, so calls can be captured, and calls that share
-    one MxLinear must not overlap (as calls that share one Buffers)."""
+    one MxLinear must not overlap (as calls that share one Buffers). `stream`
+    quantizes the weight and owns the buffers: a call on another stream is
+    ordered behind it by the caller."""
 
     def __init__(self, weight_bf16, max_tokens: int, w_fmt: int = N.MOE_MX_E2M1, a_fmt: int = N.MOE_MX_E4M3, stream=None):
         n, k = weight_bf16.shape
         self.N, self.K, self.max_tokens, self.w_fmt, self.a_fmt = n, k, max_tokens, w_fmt, a_fmt
-        self.w_codes, self.w_sf = self._buffers(n, w_fmt, weight_bf16.device)
-        self.a_codes, self.a_sf = self._buffers(max_tokens, a_fmt, weight_bf16.device)
+        # allocated on that stream: memory that another one freed may still be
+        # written by the work in front of the free
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream)
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            self.w_codes, self.w_sf = self._buffers(n, w_fmt, weight_bf16.device)
+            self.a_codes, self.a_sf = self._buffers(max_tokens, a_fmt, weight_bf16.device)
         N.mx_quant(weight_bf16, w_fmt, self.w_codes, self.w_sf, stream)
 
     def _buffers(self, rows, fmt, device):

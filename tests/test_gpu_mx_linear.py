@@ -81,3 +81,20 @@ def test_token_counts_and_refusals():
         lin(x, out)
     with pytest.raises((ValueError, N.MoeError)):
         lin(x[:4, :32], out[:4])
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_made_on_another_stream(raw):
+    """Memory that the current stream freed with work still to come is not the weight's."""
+    rng = np.random.default_rng(8)
+    wb = _bf16(rng, (2048, 4096), 4096 ** -0.5)
+    w, side = dev(wb), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    late = torch.empty((2048, 2048), dtype=torch.uint8, device=DEV)      # the codes' size
+    torch.cuda._sleep(20_000_000)
+    late.fill_(0x77)
+    del late
+    lin = LY.MxLinear(w, 4, stream=side.cuda_stream if raw else side)
+    torch.cuda.synchronize()
+    codes, sf = M.quantize_mx(F.bf16_to_f64(wb).astype(np.float32), "e2m1")
+    assert np.array_equal(host(lin.w_codes), codes) and np.array_equal(host(lin.w_sf), sf)
