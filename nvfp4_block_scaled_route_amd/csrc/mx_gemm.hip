@@ -75,11 +75,17 @@ __device__ __forceinline__ void store_out(const MgArgs& a, int64_t t, int n, flo
 
 // ------------------------------------------------------------------ few tokens
 // Up to 32 tokens the product is a stream of the weights. A workgroup owns 16
-// columns and its 8 waves split K, so that N = 4096 columns already put a
-// workgroup on each CU and all of a column's weights are in flight at once;
-// the waves' sums are added through LDS in wave order. 16 x 16 x 128 MFMAs
+// columns (TN = 1) and its 8 waves split K, so that N = 4096 columns already put
+// a workgroup on each CU and all of a column's weights are in flight at once (4
+// or 16 waves: the same or slower); the waves' sums are added through LDS in
+// wave order. With more columns it owns 32 (TN = 2), which reads the tokens half
+// as often (64: slower, 8 x 8192 x 4096 9.2 us against 7.1). 16 x 16 x 128 MFMAs
 // with the weights as rows: a lane ends up with 4 consecutive columns of one
 // token. The tokens' codes are read by every workgroup, from the L2.
+//
+// The number of load instructions bounds it: with a load a step for the scales
+// 8 x 4096 x 4096 e4m3 x e2m1 took 5.9 us, with one for four steps 4.9 (1.9
+// TB/s); 8 x 16384 x 4096 16.8 and 12.9, and 10.6 (3.4 TB/s) with 32 columns.
 constexpr int kSkWaves = 8;
 
 template <int FMT>
@@ -96,59 +102,78 @@ __device__ __forceinline__ MxFrag<FMT> load_frag16(const uint8_t* row, int step,
     return f;
 }
 
-template <int FA, int FW, int TM, bool ALIGNED>
+template <int FA, int FW, int TM, int TN, bool ALIGNED>
 __global__ void __launch_bounds__(64 * kSkWaves) mx_gemm_skinny_kernel(MgArgs a) {
     constexpr int U = 4;                    // steps whose loads issue together
-    __shared__ floatx4 s_sum[kSkWaves][TM][64];
+    __shared__ floatx4 s_sum[kSkWaves][TM * TN][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-    const int n0 = blockIdx.x * 16, nb = a.K >> 5;
-    const int nrow = n0 + r < a.N ? n0 + r : a.N - 1;
-    const uint8_t* wrow = a.w + nrow * mx_bytes(a.K, FW);
-    const uint8_t* wsf = a.w_sf + (int64_t)nrow * nb;
-    const uint8_t *arow[TM], *asf[TM];
+    const int n0 = blockIdx.x * (16 * TN), nb = a.K >> 5;
+    const uint8_t *wrow[TN], *wsf[TN], *arow[TM], *asf[TM];
+#pragma unroll
+    for (int n = 0; n < TN; ++n) {
+        const int row = n0 + 16 * n + r < a.N ? n0 + 16 * n + r : a.N - 1;
+        wrow[n] = a.w + row * mx_bytes(a.K, FW);
+        wsf[n] = a.w_sf + (int64_t)row * nb;
+    }
 #pragma unroll
     for (int m = 0; m < TM; ++m) {
         const int t = 16 * m + r < a.T ? 16 * m + r : a.T - 1;
         arow[m] = a.a + t * mx_bytes(a.K, FA);
         asf[m] = a.a_sf + (int64_t)t * nb;
     }
-    floatx4 acc[TM];
+    floatx4 acc[TM][TN];
 #pragma unroll
-    for (int m = 0; m < TM; ++m) acc[m] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int m = 0; m < TM; ++m)
+#pragma unroll
+        for (int n = 0; n < TN; ++n) acc[m][n] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
     const int steps = (a.K + 127) / 128, per = (steps + kSkWaves - 1) / kSkWaves;
     const int s0 = wave * per, s1 = s0 + per < steps ? s0 + per : steps;
     for (int s = s0; s < s1; s += U) {
-        MxFrag<FW> fw[U];
+        MxFrag<FW> fw[U][TN];
         MxFrag<FA> fa[U][TM];
-        uint32_t sw[U], sa[U][TM];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             // steps behind s1 belong to the next wave: zeros here
             const int lim = s + u < s1 ? nb : 0, limk = s + u < s1 ? a.K : 0;
-            fw[u] = load_frag16<FW>(wrow, s + u, g, lim, limk);
-            sw[u] = scale_word<ALIGNED>(wsf, 4 * (s + u), lim);
 #pragma unroll
-            for (int m = 0; m < TM; ++m) {
-                fa[u][m] = load_frag16<FA>(arow[m], s + u, g, lim, limk);
-                sa[u][m] = scale_word<ALIGNED>(asf[m], 4 * (s + u), lim);
-            }
+            for (int n = 0; n < TN; ++n) fw[u][n] = load_frag16<FW>(wrow[n], s + u, g, lim, limk);
+#pragma unroll
+            for (int m = 0; m < TM; ++m) fa[u][m] = load_frag16<FA>(arow[m], s + u, g, lim, limk);
         }
+        // The scales of U steps in one load a row: lane group g takes step s + g's
+        // four and hands them round.
+        static_assert(U == 4, "a step a lane group");
+        const int lim = s + g < s1 ? nb : 0;
+        uint32_t xw[TN], xa[TM];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int n = 0; n < TN; ++n) xw[n] = scale_word<ALIGNED>(wsf[n], 4 * (s + g), lim);
+#pragma unroll
+        for (int m = 0; m < TM; ++m) xa[m] = scale_word<ALIGNED>(asf[m], 4 * (s + g), lim);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            int sw[TN], sa[TM];
+#pragma unroll
+            for (int n = 0; n < TN; ++n) sw[n] = (int)((uint32_t)__builtin_amdgcn_ds_bpermute(4 * (16 * u + r), (int)xw[n]) >> (8 * g));
+#pragma unroll
+            for (int m = 0; m < TM; ++m) sa[m] = (int)((uint32_t)__builtin_amdgcn_ds_bpermute(4 * (16 * u + r), (int)xa[m]) >> (8 * g));
 #pragma unroll
             for (int m = 0; m < TM; ++m)
-                acc[m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    fw[u].reg(), fa[u][m].reg(), acc[m], mfma_fmt<FW>(), mfma_fmt<FA>(), 0,
-                    (int)(sw[u] >> (8 * g)), 0, (int)(sa[u][m] >> (8 * g)));
+#pragma unroll
+                for (int n = 0; n < TN; ++n)
+                    acc[m][n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        fw[u][n].reg(), fa[u][m].reg(), acc[m][n], mfma_fmt<FW>(), mfma_fmt<FA>(), 0, sw[n], 0, sa[m]);
+        }
     }
 #pragma unroll
-    for (int m = 0; m < TM; ++m) s_sum[wave][m][lane] = acc[m];
+    for (int m = 0; m < TM; ++m)
+#pragma unroll
+        for (int n = 0; n < TN; ++n) s_sum[wave][m * TN + n][lane] = acc[m][n];
     __syncthreads();
-    if (wave >= TM) return;
+    if (wave >= TM * TN) return;
     floatx4 sum = s_sum[0][wave][lane];
 #pragma unroll
     for (int w = 1; w < kSkWaves; ++w) sum += s_sum[w][wave][lane];
-    const int t = 16 * wave + r, n = n0 + 4 * g;
+    const int t = 16 * (wave / TN) + r, n = n0 + 16 * (wave % TN) + 4 * g;
     if (t >= a.T) return;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -538,13 +563,19 @@ void launch_mx_tiled(const MgArgs& a, hipStream_t s) {
 template <int FA, int FW, bool ALIGNED>
 int launch_mx_gemm(const MgArgs& a, hipStream_t s) {
     const char* name = "mx_gemm";
-    // K = N = 4096, e4m3 x e2m1: 32 tokens 9.7 us by columns, 10.6 in 64-wide
-    // blocks; 64 tokens 15.6 and 11.0
+    // K = N = 4096, e4m3 x e2m1: 32 tokens 7.9 us by columns, 10.6 in 64-wide
+    // blocks; 64 tokens (when 32 took 9.7) 15.6 and 11.0
     if (a.T <= 32) {
-        const dim3 g((unsigned)(((int64_t)a.N + 15) / 16)), b(64 * kSkWaves);
+        // 32 columns a workgroup where 16 would be more than one a CU (K = 4096, e4m3 x e2m1, 16 and 32
+        // columns: 8 tokens, N = 4096 4.9 and 6.3, 4224 7.1 and 6.3, 8192 7.9 and 7.0; 32 tokens,
+        // 4096 7.9 and 9.3, 4608 13.0 and 9.5, 16384 23.5 and 17.7)
+        const bool wide = a.N > 16 * 256;
+        const dim3 g((unsigned)(((int64_t)a.N + (wide ? 31 : 15)) / (wide ? 32 : 16))), b(64 * kSkWaves);
         if (!launch_fits(g.x, b.x)) return fail(MOE_EUNSUPPORTED, "%s: too many columns", name);
-        if (a.T <= 16) hipLaunchKernelGGL((mx_gemm_skinny_kernel<FA, FW, 1, ALIGNED>), g, b, 0, s, a);
-        else hipLaunchKernelGGL((mx_gemm_skinny_kernel<FA, FW, 2, ALIGNED>), g, b, 0, s, a);
+        if (a.T <= 16 && wide) hipLaunchKernelGGL((mx_gemm_skinny_kernel<FA, FW, 1, 2, ALIGNED>), g, b, 0, s, a);
+        else if (a.T <= 16) hipLaunchKernelGGL((mx_gemm_skinny_kernel<FA, FW, 1, 1, ALIGNED>), g, b, 0, s, a);
+        else if (wide) hipLaunchKernelGGL((mx_gemm_skinny_kernel<FA, FW, 2, 2, ALIGNED>), g, b, 0, s, a);
+        else hipLaunchKernelGGL((mx_gemm_skinny_kernel<FA, FW, 2, 1, ALIGNED>), g, b, 0, s, a);
         return check_launch(name);
     }
     const auto tiles = [&](int64_t bm, int64_t bn) { return (a.T + bm - 1) / bm * ((a.N + bn - 1) / bn); };

@@ -188,6 +188,14 @@ def test_gemm_shapes(T, Nn, K, af, wf):
     _check_gemm(T, Nn, K, af, wf)
 
 
+@pytest.mark.parametrize("af,wf", FORMATS)
+@pytest.mark.parametrize("T", [1, 16, 29])
+@pytest.mark.parametrize("Nn,K", [(4096, 160), (4097, 160), (4111, 512), (4128, 1056), (4130, 640), (8200, 96)])
+def test_gemm_few_tokens_many_columns(T, Nn, K, af, wf):
+    """Both numbers of columns a workgroup, with whole and ragged last ones."""
+    _check_gemm(T, Nn, K, af, wf)
+
+
 @pytest.mark.parametrize("T,Nn,K,pad", [(1, 5, 64, 3), (40, 37, 160, 0), (64, 64, 512, 8), (100, 70, 320, 1), (129, 72, 512, 8),
                                         (70, 64, 4096, 0)])
 def test_gemm_fp32_output_and_strides(T, Nn, K, pad):
