@@ -557,8 +557,10 @@ int mx_add_norm_quant(const uint16_t* x, int64_t x_row_stride, const uint16_t* r
  * products is exact to fp32; where an operand is e4m3 the matrix cores cut each
  * product to 13 bits below the exponent of the largest of its 8, about 1.5e-5 of
  * the result. A NaN
- * scale or e4m3 NaN code makes the row or column NaN. K % 32 == 0, K <= MOE_MAX_MX_K; any T and
- * N. One launch on `stream`, no workspace. */
+ * scale or e4m3 NaN code makes the row or column NaN. Scales are loaded in
+ * whole aligned 4-byte words, the one with the array's last byte too; what lies
+ * behind it is not used. K % 32 == 0, K <= MOE_MAX_MX_K; any T and N. One launch
+ * on `stream`, no workspace. */
 int mx_gemm(const uint8_t* a_codes, const uint8_t* a_sf, int a_fmt, const uint8_t* w_codes, const uint8_t* w_sf,
             int w_fmt, int T, int N, int K, void* out, int64_t out_row_stride, int out_dtype, void* stream);
 

@@ -206,12 +206,13 @@ __global__ void __launch_bounds__(64 * kSkWaves) mx_gemm_skinny_kernel(MgArgs a)
 
 // A row's scales travel in chunks: 32 of them (1024 elements) as two 16-byte
 // pieces where their words are aligned (K / 32 a multiple of 4, at least 16),
-// else 16 as one byte a lane, each into a word. Every stage's own few bytes
-// would touch as many cache lines as the codes do.
+// else 24 (768 elements) as the 8 aligned words from the one that holds the
+// chunk's first byte; the last such word of the array may reach 3 bytes past it.
+// Every stage's own few bytes would touch as many cache lines as the codes do.
 // PIECES: of an aligned chunk.
 template <int PIECES, bool ALIGNED>
 struct MgScale {
-    static constexpr int kBytes = ALIGNED ? 16 * PIECES : 16, kRow = ALIGNED ? 16 * PIECES : 64;      // of a row, in memory and in LDS
+    static constexpr int kBytes = ALIGNED ? 16 * PIECES : 24, kRow = ALIGNED ? 16 * PIECES : 32;      // of a row, in memory and in LDS
 };
 
 template <int FA, int FW, int MW, int NW, bool ALIGNED>
@@ -249,9 +250,9 @@ __device__ __forceinline__ int mg_swizzle(int chunk, int row) {
     else return chunk ^ ((row >> 2) & 3);
 }
 
-// Direct-to-LDS load of one byte a lane into a word, as lds_copy16.
-__device__ __forceinline__ void lds_copy1(u32x4 rsrc, uint32_t lds, uint32_t voff, uint32_t soff) {
-    asm volatile("buffer_load_ubyte %0, %1, %2 offen lds" :: "v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds) : "memory");
+// Direct-to-LDS load of one word a lane, as lds_copy16.
+__device__ __forceinline__ void lds_copy4(u32x4 rsrc, uint32_t lds, uint32_t voff, uint32_t soff) {
+    asm volatile("buffer_load_dword %0, %1, %2 offen lds" :: "v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds) : "memory");
 }
 
 // One operand's codes: instruction q of a wave copies 1 KB, the rows
@@ -282,33 +283,49 @@ struct MgCopy {
     }
 };
 
-// One operand's scales. Blocks of few rows take less than one instruction a
-// wave: waves then repeat each other's.
+// One operand's scales, aligned. Blocks of few rows take less than one
+// instruction a wave: waves then repeat each other's.
 template <int ROWS, int PIECES, bool ALIGNED>
 struct MgScaleCopy {
-    static constexpr int kLanes = ALIGNED ? PIECES : 16, kRowsPer = 64 / kLanes, kParts = ROWS / kRowsPer;
-    static constexpr int kCopies = kParts > 4 ? kParts / 4 : 1;
+    static constexpr int kRowsPer = 64 / PIECES, kParts = ROWS / kRowsPer, kCopies = kParts > 4 ? kParts / 4 : 1;
     u32x4 rsrc;
     uint32_t off[kCopies];  // of a lane's rows
     __device__ __forceinline__ void init(const uint8_t* base, int nb, int rows_left, int wave, int lane) {
         rsrc = buffer_desc(base);
 #pragma unroll
         for (int q = 0; q < kCopies; ++q) {
-            const int r = kRowsPer * ((4 * q + wave) % kParts) + lane / kLanes;
+            const int r = kRowsPer * ((4 * q + wave) % kParts) + lane / PIECES;
             off[q] = (uint32_t)((r < rows_left ? r : rows_left - 1) * nb);
         }
     }
     // Chunk c into LDS at lds. The piece that would pass the row's end lies
-    // against it instead (mg_scales goes by that); bytes behind it are zeros.
+    // against it instead (MgScales goes by that).
     __device__ __forceinline__ void issue(uint32_t lds, int c, int wave, int lane, int nb) const {
-        const int b = ALIGNED ? 16 * (PIECES * c + lane % PIECES) : 16 * c + lane % 16;
-        const int at = !ALIGNED ? b : b < nb - 16 ? b : nb - 16;
+        const int b = 16 * (PIECES * c + lane % PIECES), at = b < nb - 16 ? b : nb - 16;
 #pragma unroll
-        for (int q = 0; q < kCopies; ++q) {
-            const uint32_t to = __builtin_amdgcn_readfirstlane(lds + (4 * q + wave) % kParts * (ALIGNED ? 1024 : 256));
-            if constexpr (ALIGNED) lds_copy16(rsrc, to, off[q] + at, 0u);
-            else lds_copy1(rsrc, to, b < nb ? off[q] + at : 0x80000000u, 0u);
-        }
+        for (int q = 0; q < kCopies; ++q)
+            lds_copy16(rsrc, __builtin_amdgcn_readfirstlane(lds + (4 * q + wave) % kParts * 1024), off[q] + at, 0u);
+    }
+};
+
+// Not aligned: 8 lanes a row, each a word. Words behind a row's last scale and
+// rows behind the last are zeros.
+template <int ROWS, int PIECES>
+struct MgScaleCopy<ROWS, PIECES, false> {
+    u32x4 rsrc;
+    uint32_t off;           // of a lane's first row's first word
+    int row, left, skew;    // that row, the rows there are, the byte of the word at which the row starts
+    __device__ __forceinline__ void init(const uint8_t* base, int nb, int rows_left, int wave, int lane) {
+        rsrc = buffer_desc(base);
+        row = 8 * wave + lane / 8, left = rows_left;
+        off = (uint32_t)(row * nb) & ~3u, skew = row * nb & 3;
+    }
+    __device__ __forceinline__ void issue(uint32_t lds, int c, int wave, int lane, int nb) const {
+        const int b = 24 * c + 4 * (lane % 8), end = b < nb + skew ? left : 0;
+#pragma unroll
+        for (int q = 0; q < ROWS / 32; ++q)     // 32 rows are whole words
+            lds_copy4(rsrc, __builtin_amdgcn_readfirstlane(lds + (4 * q + wave) * 256),
+                      row + 32 * q < end ? off + b : 0x80000000u, (uint32_t)(32 * q * nb));
     }
 };
 
@@ -331,13 +348,14 @@ __device__ __forceinline__ MxFrag<FMT> mg_read(const uint8_t* rows, int row, int
 // A stage's scales of a lane's row. read() takes what LDS holds and scales() makes
 // one register of it, step s's byte at s, or with 2 steps at 2 s, zeros behind
 // the row's nb blocks: apart, so that no instruction waits for the LDS between
-// the reads and the MFMAs that cover them. b0: the stage's first block.
+// the reads and the MFMAs that cover them. b0: the stage's first block, c0: the
+// chunk's. Not aligned, a row starts at byte `skew` of its first word.
 template <int STEPS, bool PAIR, int PIECES, bool ALIGNED>
 struct MgScales {
     static constexpr int kWords = PAIR && STEPS == 4 ? 2 : 1;       // of 4 blocks each
-    uint4 raw[kWords];                                              // aligned: x alone
+    uint2 raw[kWords];                                              // aligned: x alone
     __device__ __forceinline__ static int block(int b0, int i, int g) { return b0 + 4 * (PAIR ? i : g); }
-    __device__ __forceinline__ void read(const uint8_t* row, int b0, int nb, int g) {
+    __device__ __forceinline__ void read(const uint8_t* row, int b0, int c0, int nb, int g) {
 #pragma unroll
         for (int i = 0; i < kWords; ++i) {
             const int b = block(b0, i, g);
@@ -345,16 +363,22 @@ struct MgScales {
                 const int piece = b & ~15, at = piece < nb - 16 ? piece : nb - 16;
                 raw[i].x = *reinterpret_cast<const uint32_t*>(row + (PIECES == 2 ? b & 16 : 0) + (b < nb ? b - at : 0));
             } else {
-                raw[i] = *reinterpret_cast<const uint4*>(row + (b & 15) * 4);
+                const uint32_t* w = reinterpret_cast<const uint32_t*>(row + (b - c0));
+                raw[i] = make_uint2(w[0], w[1]);
             }
         }
     }
-    __device__ __forceinline__ uint32_t scales(int b0, int nb, int g) const {
+    __device__ __forceinline__ uint32_t scales(int b0, int nb, int g, int skew) const {
         uint32_t v[kWords];
 #pragma unroll
         for (int i = 0; i < kWords; ++i) {
-            if constexpr (ALIGNED) v[i] = block(b0, i, g) < nb ? raw[i].x : 0u;
-            else v[i] = raw[i].x | (raw[i].y << 8) | (raw[i].z << 16) | (raw[i].w << 24);
+            const int left = nb - block(b0, i, g);
+            if constexpr (ALIGNED) {
+                v[i] = left > 0 ? raw[i].x : 0u;
+            } else {        // the next row's bytes among them
+                const uint32_t w = __builtin_amdgcn_alignbyte(raw[i].y, raw[i].x, skew);
+                v[i] = left >= 4 ? w : left > 0 ? w & ((1u << (8 * left)) - 1u) : 0u;
+            }
         }
         if constexpr (!PAIR) return v[0];                               // blocks 4 g + step
         else if constexpr (STEPS == 2) return v[0] >> (8 * g);          // blocks g, 2 + g
@@ -461,18 +485,20 @@ __global__ void __launch_bounds__(256, (MgShape<FA, FW, MW, NW, ALIGNED>::kPerCu
     using Scales = MgScales<S::kSteps, kPair, S::kPieces, ALIGNED>;
     Scales na[MW], nw[NW];      // the next stage's, as read
     uint32_t sa[MW], sw[NW];
+    const int skew = r * nb & 3;        // 32 rows are whole words
     auto read_scales = [&](int s) {
+        const int c0 = s / S::kSpc * Sf::kBytes;
         const uint8_t* at = lds + S::kSf + (s / S::kSpc & 1) * S::kChunk;
 #pragma unroll
-        for (int m = 0; m < MW; ++m) na[m].read(at + Sf::kRow * (32 * (wm * MW + m) + r), s * (S::kElems / 32), nb, g);
+        for (int m = 0; m < MW; ++m) na[m].read(at + Sf::kRow * (32 * (wm * MW + m) + r), s * (S::kElems / 32), c0, nb, g);
 #pragma unroll
-        for (int n = 0; n < NW; ++n) nw[n].read(at + Sf::kRow * (S::kBM + 32 * (wn * NW + n) + r), s * (S::kElems / 32), nb, g);
+        for (int n = 0; n < NW; ++n) nw[n].read(at + Sf::kRow * (S::kBM + 32 * (wn * NW + n) + r), s * (S::kElems / 32), c0, nb, g);
     };
     auto take_scales = [&](int s) {
 #pragma unroll
-        for (int m = 0; m < MW; ++m) sa[m] = na[m].scales(s * (S::kElems / 32), nb, g);
+        for (int m = 0; m < MW; ++m) sa[m] = na[m].scales(s * (S::kElems / 32), nb, g, skew);
 #pragma unroll
-        for (int n = 0; n < NW; ++n) sw[n] = nw[n].scales(s * (S::kElems / 32), nb, g);
+        for (int n = 0; n < NW; ++n) sw[n] = nw[n].scales(s * (S::kElems / 32), nb, g, skew);
     };
     struct Operands {
         MxFrag<FA> a[MW];
@@ -586,14 +612,17 @@ int launch_mx_gemm(const MgArgs& a, hipStream_t s) {
     //   517 x 2048 e4m3 x e2m1   16.0  16.9  28.4  53.6     1024 x 4096  30.0  23.0  29.9  53.8
     //   1536 x 4096 e4m3 x e2m1  43.8  36.1  32.9  54.1     2048 x 4096  57.2  42.9  37.3  53.8
     //   1536 x 4096 e2m1         31.9  28.6  22.7  36.6     2800 x 4096  55.4  46.5  38.5  37.6
-    // (rows of scales that are not aligned leave LDS for blocks up to 128 x 128)
-    if constexpr (ALIGNED) {
-        if (tiles(256, 256) >= 168) {
-            launch_mx_tiled<FA, FW, 4, 4, ALIGNED>(a, s);
-            return check_launch(name);
-        }
-    }
-    if (tiles(128, 128) >= 320) launch_mx_tiled<FA, FW, 2, 2, ALIGNED>(a, s);
+    // 256 x 256, a workgroup a CU, where the last round of them is filled; us, 128 x 128 and 256 x 256,
+    // N = K = 4096, e2m1, by the blocks of 256 x 256:
+    //   176  39.0  38.8    224  42.5  38.0    256  45.3  39.9    304  56.0  70.2    352  62.6  70.8
+    //   400  75.9  71.8    512  87.9  77.4;   with K = 4128  208  53.9  49.6    256  62.2  51.3
+    // (not e4m3 x e4m3 with scales that are not aligned, whose registers do not suffice: 4096 x 4096 x
+    // 4128 160.6 us against 102.9)
+    constexpr bool kWidest = ALIGNED || FW == MOE_MX_E2M1;
+    const int64_t widest = tiles(256, 256), last = (widest - 1) % 256 + 1;
+    if (kWidest && last >= (widest <= 256 ? 168 : 128))
+        launch_mx_tiled<FA, FW, kWidest ? 4 : 2, kWidest ? 4 : 2, ALIGNED>(a, s);
+    else if (tiles(128, 128) >= 320) launch_mx_tiled<FA, FW, 2, 2, ALIGNED>(a, s);
     else if (tiles(64, 64) > 512) launch_mx_tiled<FA, FW, 1, 2, ALIGNED>(a, s);
     else launch_mx_tiled<FA, FW, 1, 1, ALIGNED>(a, s);
     return check_launch(name);

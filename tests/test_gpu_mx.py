@@ -221,6 +221,14 @@ def test_gemm_each_block_size(T, Nn, K, af, wf):
 
 
 @pytest.mark.parametrize("af,wf", FORMATS)
+@pytest.mark.parametrize("T,Nn", [(130, 200), (1030, 2200), (1700, 3300), (2817, 3841)])
+@pytest.mark.parametrize("K", [1056, 2112, 2144])
+def test_gemm_each_block_size_with_odd_rows_of_scales(T, Nn, K, af, wf):
+    """The same where rows of scales start at each byte of a word, in three chunks of them."""
+    _check_gemm(T, Nn, K, af, wf)
+
+
+@pytest.mark.parametrize("af,wf", FORMATS)
 @pytest.mark.parametrize("K", [1024, 1056, 2176, 4128, 8320])
 def test_gemm_many_stages(K, af, wf):
     """Rings and chunks of scales that wrap round many times."""
@@ -258,6 +266,25 @@ def test_gemm_e4m3_nan_codes(T):
         nan = np.zeros((T, 70), bool)
         nan[2], nan[4], nan[:, 69] = True, True, True
         assert np.array_equal(np.isnan(_gemm(ac, asf, "e4m3", wc, wsf, "e4m3")), nan)
+
+
+@pytest.mark.parametrize("T", [5, 70, 333])
+@pytest.mark.parametrize("K", [96, 160, 992])
+def test_gemm_bytes_behind_the_scales(T, K):
+    """The scales' array may be followed by anything: NaN scales behind it reach nothing."""
+    rng = np.random.default_rng(T + K)
+    Nn = 67
+    (ac, asf), (wc, wsf) = _values(rng, T, K, "e4m3"), _values(rng, Nn, K, "e2m1")
+
+    def inside(sf):
+        buf = torch.full((sf.size + 64,), 255, dtype=torch.uint8, device=DEV)
+        buf[:sf.size] = dev(sf).reshape(-1)
+        return buf[:sf.size].view(sf.shape)
+
+    out = torch.empty((T, Nn), dtype=torch.bfloat16, device=DEV)
+    N.mx_gemm(dev(ac), inside(asf), N.MOE_MX_E4M3, dev(wc), inside(wsf), N.MOE_MX_E2M1, out)
+    torch.cuda.synchronize()
+    assert np.array_equal(out.float().cpu().numpy(), _gemm(ac, asf, "e4m3", wc, wsf, "e2m1"))
 
 
 def test_gemm_e2m1_products_are_exact():
