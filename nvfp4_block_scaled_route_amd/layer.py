@@ -75,7 +75,7 @@ class MxLinear:
         # allocated on that stream: memory that another one freed may still be
         # written by the work in front of the free
         if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream)
+            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
         with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
             self.w_codes, self.w_sf = self._buffers(n, w_fmt, weight_bf16.device)
             self.a_codes, self.a_sf = self._buffers(max_tokens, a_fmt, weight_bf16.device)

@@ -98,3 +98,18 @@ def test_made_on_another_stream(raw):
     torch.cuda.synchronize()
     codes, sf = M.quantize_mx(F.bf16_to_f64(wb).astype(np.float32), "e2m1")
     assert np.array_equal(host(lin.w_codes), codes) and np.array_equal(host(lin.w_sf), sf)
+
+
+def test_made_on_the_null_stream():
+    """Raw stream 0 is the default one: behind the work that makes the weight there."""
+    rng = np.random.default_rng(9)
+    wb = _bf16(rng, (256, 1024), 2.0 ** -5)
+    w, made, side = torch.zeros((256, 1024), dtype=torch.int16, device=DEV), dev(wb), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    w.copy_(made)
+    with torch.cuda.stream(side):
+        lin = LY.MxLinear(w, 4, stream=0)
+    torch.cuda.synchronize()
+    codes, sf = M.quantize_mx(F.bf16_to_f64(wb).astype(np.float32), "e2m1")
+    assert np.array_equal(host(lin.w_codes), codes) and np.array_equal(host(lin.w_sf), sf)
