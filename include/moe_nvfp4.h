@@ -533,6 +533,8 @@ int mx_dequant(const uint8_t* codes, const uint8_t* sf, int T, int H, int fmt, u
  *   h_j = bf16(x_j + residual_j)      (the fp32 sum, rounded; h = x with no residual)
  *   s   = sum_j h_j^2 in fp64;  ms = fp32(s / H);  r = 1 / sqrt(ms + eps)
  *   y_j = (h_j * r) * gamma_j,  gamma_j = fp32(norm_weight_j) + gain_center
+ *   (a finite row with s / H past fp32's range: r and h_j * r in fp64, the latter
+ *   rounded to fp32)
  *   y -> MX codes and scales (a row that holds a NaN or an infinity: every block NaN)
  *   x            device bf16 [T, H], row stride x_row_stride elements
  *   residual     device bf16 [T, H], or NULL
