@@ -192,9 +192,11 @@ __global__ void __launch_bounds__(1024) add_norm_kernel(AnArgs a) {
     // A finite row may have a mean square past fp32's range (values above 1.8e19):
     // its reciprocal root is below fp32's normal numbers, so h * r is formed in
     // fp64 and rounded once. A branch of the wave: both ways for every element
-    // cost 5% (4096 x 4096 21.0 -> 22.1 us).
+    // cost 5% (4096 x 4096 21.0 -> 22.1 us). A row that holds an infinity is NaN
+    // throughout, like one that holds a NaN: h / infinity would leave zeros, which
+    // no later step tells from values.
     if (__builtin_amdgcn_readfirstlane(ms == INFINITY)) {
-        const double rd = __ddiv_rn(1.0, sqrt(__dadd_rn(mean, (double)a.eps)));
+        const double rd = mean == (double)INFINITY ? (double)NAN : __ddiv_rn(1.0, sqrt(__dadd_rn(mean, (double)a.eps)));
         store([&](float x) { return __double2float_rn(__dmul_rn((double)x, rd)); });
     } else {
         store([&](float x) { return __fmul_rn(x, rr); });

@@ -53,7 +53,8 @@ def add_norm_mx(x_bf16, residual_bf16, norm_weight_bf16, gain_center: float, eps
     """bf16 bits [T, H] -> (sum bf16 bits, codes, scale bytes): the sum rounded
     to bf16 from its fp32 rounding, then the norm of those values step by step
     in fp32 (the mean square from an exact fp64 sum), then quantize_mx. Where the
-    mean square passes fp32's range, r and h * r are formed in fp64."""
+    mean square passes fp32's range, r and h * r are formed in fp64; r is NaN for
+    a row that holds an infinity."""
     x = bf16_to_f64(x_bf16)
     if residual_bf16 is not None:
         with np.errstate(over="ignore", invalid="ignore"):
@@ -65,7 +66,7 @@ def add_norm_mx(x_bf16, residual_bf16, norm_weight_bf16, gain_center: float, eps
         s = (v.astype(np.float64) ** 2).sum(axis=1, dtype=np.longdouble).astype(np.float64)
         ms = (s / H).astype(np.float32)
         r = (np.float32(1.0) / np.sqrt(ms + np.float32(eps)).astype(np.float32)).astype(np.float32)
-        rd = 1.0 / np.sqrt(s / H + np.float64(np.float32(eps)))
+        rd = np.where(np.isinf(s), np.nan, 1.0 / np.sqrt(s / H + np.float64(np.float32(eps))))
         n = np.where(np.isinf(ms)[:, None], (v.astype(np.float64) * rd[:, None]).astype(np.float32), v * r[:, None])
         y = n * gamma(norm_weight_bf16, gain_center, H)[None, :]
     codes, sf = quantize_mx(y.astype(np.float32), fmt)

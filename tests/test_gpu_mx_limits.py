@@ -41,3 +41,21 @@ def test_finite_rows_of_any_size_are_normalized(H, fmt):
     for r, w, center in ((None, None, 0.0), (rb, wb, 1.0)):
         h, codes, sf = _norm(xb, r, w, center, 1e-6, fmt)
         assert_codes_near(codes, sf, norm64(h, w, center, 1e-6), fmt)
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("H", [32, 128, 4096, 16384])
+def test_a_row_with_an_infinity_or_a_nan_is_nan_in_every_block(H, fmt):
+    """In x, in the residual, or made by their sum; the rows beside are not touched."""
+    rng = np.random.default_rng(H)
+    a, b = (rng.standard_normal((9, H)).astype(np.float32) for _ in range(2))
+    a[1, 0], a[2, H - 1], b[3, H // 2], a[4, 7], b[5, 3] = np.inf, -np.inf, np.inf, np.nan, np.nan
+    a[6, 9] = b[6, 9] = 3e38                        # their sum is infinite
+    a[7, 1], b[7, 1] = np.inf, -np.inf              # theirs NaN
+    wb = F.f32_to_bf16((rng.standard_normal(H) * 0.1).astype(np.float32))
+    for w, center in ((None, 0.0), (wb, 1.0)):
+        _, codes, sf = _norm(F.f32_to_bf16(a), F.f32_to_bf16(b), w, center, 1e-6, fmt)
+        assert (sf[1:8] == 255).all() and not codes[1:8].any()
+        assert (sf[[0, 8]] != 255).all()
+    _, codes, sf = _norm(F.f32_to_bf16(a), None, wb, 1.0, 1e-6, fmt)
+    assert (sf[[1, 2, 4, 7]] == 255).all() and (sf[[0, 3, 5, 6, 8]] != 255).all()

@@ -19,3 +19,16 @@ def test_finite_rows_of_any_size_are_normalized(size, fmt):
         h, codes, sf = M.add_norm_mx(xb, None, w, center, 1e-6, fmt)
         assert np.array_equal(h, xb)
         assert_codes_near(codes, sf, norm64(xb, w, center, 1e-6), fmt)
+
+
+BAD = [(0, np.inf), (5, -np.inf), (100, np.nan), (255, np.inf)]
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+def test_a_row_with_an_infinity_or_a_nan_is_nan_in_every_block(fmt):
+    x = np.random.default_rng(4).standard_normal((6, 256)).astype(np.float32)
+    for t, (j, v) in enumerate(BAD):
+        x[t, j] = v
+    _, codes, sf = M.add_norm_mx(F.f32_to_bf16(x), None, None, 0.0, 1e-6, fmt)
+    assert (sf[:4] == 255).all() and not codes[:4].any()
+    assert (sf[4:] != 255).all()
