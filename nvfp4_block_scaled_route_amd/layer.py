@@ -71,6 +71,7 @@ class MxLinear:
 
     def __init__(self, weight_bf16, max_tokens: int, w_fmt: int = N.MOE_MX_E2M1, a_fmt: int = N.MOE_MX_E4M3, stream=None):
         n, k = weight_bf16.shape
+        N.mx_gemm_validate(a_fmt, w_fmt, n, k)      # here, not at the first call
         self.N, self.K, self.max_tokens, self.w_fmt, self.a_fmt = n, k, max_tokens, w_fmt, a_fmt
         # allocated on that stream: memory that another one freed may still be
         # written by the work in front of the free

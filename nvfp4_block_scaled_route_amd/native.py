@@ -450,6 +450,12 @@ def mx_gemm(a_codes, a_sf, a_fmt, w_codes, w_sf, w_fmt, out, stream=None) -> Non
         _check(rc, call)
 
 
+def mx_gemm_validate(a_fmt, w_fmt, N, K) -> None:
+    """Host-only check that mx_gemm takes these formats and K; raises MoeError. (A
+    call of no tokens: it checks them, reads nothing and launches nothing.)"""
+    _check(lib().mx_gemm(None, None, a_fmt, None, None, w_fmt, 0, N, K, None, N, MOE_BF16, None), "mx_gemm")
+
+
 def _row_type(call, rows) -> int:
     if rows.dtype == torch.float32:
         return MOE_F32
