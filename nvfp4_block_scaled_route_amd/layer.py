@@ -66,8 +66,9 @@ class MxLinear:
     weight [N, K] (bf16) quantized once, x per call. Holds the buffers of calls
     with up to max_tokens rows, so calls can be captured, and calls that share
     one MxLinear must not overlap (as calls that share one Buffers). `stream`
-    quantizes the weight and owns the buffers: a call on another stream is
-    ordered behind it by the caller."""
+    quantizes the weight, behind what makes the weight there by the caller's order,
+    and owns the buffers: a call on another stream is ordered behind it, and ends
+    before the last reference to the MxLinear goes, by the caller's order too."""
 
     def __init__(self, weight_bf16, max_tokens: int, w_fmt: int = N.MOE_MX_E2M1, a_fmt: int = N.MOE_MX_E4M3, stream=None):
         n, k = weight_bf16.shape
@@ -81,6 +82,8 @@ class MxLinear:
             self.w_codes, self.w_sf = self._buffers(n, w_fmt, weight_bf16.device)
             self.a_codes, self.a_sf = self._buffers(max_tokens, a_fmt, weight_bf16.device)
         N.mx_quant(weight_bf16, w_fmt, self.w_codes, self.w_sf, stream)
+        if stream is not None:      # the caller may drop the weight while that stream still reads it
+            weight_bf16.record_stream(stream)
 
     def _buffers(self, rows, fmt, device):
         width = self.K // 2 if fmt == N.MOE_MX_E2M1 else self.K
