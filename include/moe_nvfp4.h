@@ -529,7 +529,8 @@ int mx_dequant(const uint8_t* codes, const uint8_t* sf, int T, int H, int fmt, u
 
 /* The residual's addition, the RMSNorm of the sum, and its MX codes, in one
  * pass (the model page, "MuseSpark1xDecoderLayer": a residual boundary; the
- * norm's arithmetic is nvfp4_norm_quant's). Per row of H values:
+ * norm's steps are nvfp4_norm_quant's, the root correctly rounded). Per row of H
+ * values:
  *   h_j = bf16(x_j + residual_j)      (the fp32 sum, rounded; h = x with no residual)
  *   s   = sum_j h_j^2 in fp64;  ms = fp32(s / H);  r = 1 / sqrt(ms + eps)
  *   y_j = (h_j * r) * gamma_j,  gamma_j = fp32(norm_weight_j) + gain_center
@@ -555,13 +556,12 @@ int mx_add_norm_quant(const uint16_t* x, int64_t x_row_stride, const uint16_t* r
  *   w_codes, w_sf  device: MX [N, K], w_fmt (row-major, as mx_quant writes)
  *   out            device [T, N], row stride out_row_stride elements (>= N), of
  *                  type out_dtype: MOE_BF16, or MOE_F32 where both operands are e2m1
- * (a_fmt, w_fmt): (e2m1, e2m1), (e4m3, e2m1) or (e4m3, e4m3). The sum of e2m1
- * products is exact to fp32; where an operand is e4m3 the matrix cores cut each
- * product to 13 bits below the exponent of the largest of its 8, about 1.5e-5 of
- * the result. A NaN
- * scale or e4m3 NaN code makes the row or column NaN. Scales are loaded in
- * whole aligned 4-byte words, the one with the array's last byte too; what lies
- * behind it is not used. K % 32 == 0, K <= MOE_MAX_MX_K; any T and N. One launch
+ * (a_fmt, w_fmt): (e2m1, e2m1), (e4m3, e2m1) or (e4m3, e4m3). e2m1 products are
+ * added whole, and only the accumulators round; where an operand is e4m3 the
+ * matrix cores cut each product to 13 bits below the exponent of the largest of
+ * its 8, about 1.5e-5 of the result. A NaN scale or e4m3 NaN code makes the row
+ * or column NaN. Scales are loaded in whole aligned 4-byte words, the one with
+ * the array's last byte too; what lies behind it is not used. K % 32 == 0, K <= MOE_MAX_MX_K; any T and N. One launch
  * on `stream`, no workspace. */
 int mx_gemm(const uint8_t* a_codes, const uint8_t* a_sf, int a_fmt, const uint8_t* w_codes, const uint8_t* w_sf,
             int w_fmt, int T, int N, int K, void* out, int64_t out_row_stride, int out_dtype, void* stream);
@@ -582,7 +582,8 @@ int mx_gemm(const uint8_t* a_codes, const uint8_t* a_sf, int a_fmt, const uint8_
  * T or H (row_bytes) zero nothing is launched or written.
  *
  * moe_dispatch: rows[p(t,k)] = x[t], rows of any type as bytes (quantized codes
- * and scales too); row_bytes % 16 == 0, at most 4 * MOE_MAX_HIDDEN. */
+ * too, and scales where a row of them fills 16 bytes: MX, H % 512 == 0);
+ * row_bytes % 16 == 0, at most 4 * MOE_MAX_HIDDEN. */
 int moe_dispatch(const void* x, int64_t x_row_stride_bytes, int64_t row_bytes, const int32_t* exp2perm,
                  const int32_t* perm2tok, const int32_t* total_rows, int T, int K, int64_t rows_max, void* rows,
                  int64_t rows_stride_bytes, void* stream);

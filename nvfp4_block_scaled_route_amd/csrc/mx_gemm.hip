@@ -11,12 +11,16 @@
 // block g's in both. The K order is free as long as both operands and the
 // scales agree on it.
 //
-// The matrix cores sum e2m1 products exactly (into fp32 accumulators). Of 8
-// products with e4m3 values each is cut to 13 bits below the largest one's
+// The matrix cores add e2m1 products whole (into fp32 accumulators, which round
+// once a step). Of 8 products with e4m3 values each is cut to 13 bits below the largest one's
 // exponent before they are added (measured: 2^-13 beside 1 is kept, 2^-14 is
 // not), which costs about 1.5e-5 of a result (3.3e-5 where one value in a
 // hundred is an outlier): far below bf16's rounding, but not fp32's; hence no
 // fp32 output for them.
+//
+// The compiler may sink MFMAs into a divergent branch that alone uses their
+// result, where lanes are off and their operands lost: both kernels use every
+// accumulator in all lanes (a write to the LDS), and branch behind that.
 #include <type_traits>
 
 #include "experts.hpp"
@@ -200,9 +204,10 @@ __global__ void __launch_bounds__(64 * kSkWaves) mx_gemm_skinny_kernel(MgArgs a)
 // not allow; the 16-byte chunks of a row are XOR-permuted so that 16 consecutive
 // rows' reads of one chunk spread over all 64 banks.
 //
-// 4096 x 4096 x 4096: e2m1 40.5 us (3.4 PFLOP/s; the MFMAs alone 22.5 on random
-// data, where the chip's power holds the matrix unit at 6.4 PFLOP/s; on zeros the
-// whole takes 37), e4m3 x e2m1 59 to 65 us (2.2 PFLOP/s).
+// 4096 x 4096 x 4096, from one GPU to another: e2m1 39 to 43 us (3.2 to 3.5
+// PFLOP/s; the MFMAs alone 21.8 on random data, where the chip's power holds the
+// matrix unit at 6.3 PFLOP/s, and 8.5 on zeros), fp32 output 47, e4m3 x e2m1 59
+// to 65 us (2.2 PFLOP/s), e4m3 x e4m3 66.
 
 // A row's scales travel in chunks: 32 of them (1024 elements) as two 16-byte
 // pieces where their words are aligned (K / 32 a multiple of 4, at least 16),
@@ -218,9 +223,11 @@ struct MgScale {
 template <int FA, int FW, int MW, int NW, bool ALIGNED>
 struct MgShape {
     static constexpr int kBM = 64 * MW, kBN = 64 * NW;
-    // K of a stage: 256 where an operand is e2m1 (128 bytes of its rows), but for
-    // the wider blocks with e4m3 tokens, of which LDS would hold too few stages
-    // (2048 x 4096 x 4096 in 128-wide blocks: 48.3 us with 256, 41.2 with 128)
+    // K of a stage: 256 with e2m1 tokens (128 bytes of a row), and with e4m3 tokens
+    // in the blocks below 128 x 128; in the wider ones LDS would hold too few such
+    // stages (e4m3 x e2m1 2048 x 4096 x 4096 in 128-wide blocks: 48.3 us with 256,
+    // 41.2 with 128). e4m3 x e4m3 was not timed with 128 in the small blocks: its 64
+    // x 128 block with 256 takes nearly all of a CU's LDS.
     static constexpr int kElems = FA == MOE_MX_E2M1 || MW * NW < 4 ? 256 : 128;
     static constexpr int kSteps = kElems / 64;
     static constexpr int kABytes = FA == MOE_MX_E2M1 ? kElems / 2 : kElems;
@@ -236,7 +243,7 @@ struct MgShape {
     // is in flight hides the memory's latency where the blocks are small. A chunk
     // of scales overwrites the last but one, whose stages must be past (ring of
     // at most kSpc + 1).
-    static constexpr int kPerCu = MW * NW >= 8 || 2 * (2 * kStage + 2 * kChunk) > 160 * 1024 ? 1 : 2;
+    static constexpr int kPerCu = MW * NW >= 16 || 2 * (2 * kStage + 2 * kChunk) > 160 * 1024 ? 1 : 2;
     static constexpr int kFit = (160 * 1024 / kPerCu - 2 * kChunk) / kStage, kMax = kSpc + 1 < 6 ? kSpc + 1 : 6;
     static constexpr int kRing = kFit < kMax ? kFit : kMax;
     static constexpr int kSf = kRing * kStage, kLds = kSf + 2 * kChunk;
@@ -616,6 +623,10 @@ int launch_mx_gemm(const MgArgs& a, hipStream_t s) {
     // N = K = 4096, e2m1, by the blocks of 256 x 256:
     //   176  39.0  38.8    224  42.5  38.0    256  45.3  39.9    304  56.0  70.2    352  62.6  70.8
     //   400  75.9  71.8    512  87.9  77.4;   with K = 4128  208  53.9  49.6    256  62.2  51.3
+    // Both sides of these outputs were 517 or more, and e4m3 x e4m3 is not among them. The rule
+    // counts blocks and not what they hold: a thin output of many columns takes wide blocks that
+    // are mostly behind its last token (e4m3 x e2m1, K = 4096: 64 x 43008 54.7 us and 64 x 65536
+    // 59.2, where the bytes need 20 and 30).
     // (not e4m3 x e4m3 with scales that are not aligned, whose registers do not suffice: 4096 x 4096 x
     // 4128 160.6 us against 102.9)
     constexpr bool kWidest = ALIGNED || FW == MOE_MX_E2M1;

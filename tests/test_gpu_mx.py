@@ -177,6 +177,7 @@ def _check_gemm(T, Nn, K, af, wf, f32=False, pad=0, seed=0):
 
 FORMATS = [("e2m1", "e2m1"), ("e4m3", "e2m1"), ("e4m3", "e4m3")]
 # few tokens (1, 2 and 4 groups of 16), each edge of N and K; then every tile
+# (the kernel of few tokens takes 1 and 2 groups, up to 32; from 33 on it is the tiled one)
 SHAPES = [(1, 1, 32), (1, 17, 64), (2, 16, 96), (8, 100, 128), (15, 33, 160), (16, 64, 4096), (17, 40, 1056), (31, 16, 224),
           (32, 129, 512), (33, 15, 768), (64, 48, 2048), (63, 250, 4128),
           (65, 64, 32), (65, 1, 64), (70, 33, 96), (128, 64, 256), (127, 190, 288), (200, 130, 1536), (257, 300, 480)]
