@@ -316,6 +316,7 @@ _TYPED_ROWS = _BF16_TYPES + (torch.float32,)
 _U8, _I32, _F32 = (torch.uint8,), (torch.int32,), (torch.float32,)
 _E4M3_TYPES = (torch.uint8, torch.float8_e4m3fn)
 _SF_TYPES = (torch.uint8, torch.float8_e8m0fnu)
+_I32_MAX = 0x7FFFFFFF     # the library's sizes; ctypes would pass the low half of a larger one
 
 
 def _refuse(call, name, t, dtypes, shape, dev):
@@ -375,7 +376,10 @@ def _where(call, t, stream) -> tuple[int, int]:
 def _shape2(call, name, t):
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{call}: {name} must be a tensor of two dimensions")
-    return t.shape
+    shape = t.shape
+    if shape[0] > _I32_MAX or shape[1] > _I32_MAX:
+        raise MoeError(f"{call}: {name} of shape {tuple(shape)} is too large")
+    return shape
 
 
 def _mx(call, T, H, fmt, codes, sf, dev) -> tuple[int, int]:
@@ -440,6 +444,8 @@ def mx_gemm(a_codes, a_sf, a_fmt, w_codes, w_sf, w_fmt, out, stream=None) -> Non
     call = "mx_gemm"
     shape = T, N = _shape2(call, "out", out)
     K = _shape2(call, "a_sf", a_sf)[1] * 32
+    if K > _I32_MAX:
+        raise MoeError(f"{call}: K={K} is too large")
     dev, st = _where(call, out, stream)
     ld = _rows(call, "out", out, _TYPED_ROWS, shape, dev)
     a, asf = _mx(call, T, K, a_fmt, a_codes, a_sf, dev)
@@ -453,6 +459,8 @@ def mx_gemm(a_codes, a_sf, a_fmt, w_codes, w_sf, w_fmt, out, stream=None) -> Non
 def mx_gemm_validate(a_fmt, w_fmt, N, K) -> None:
     """Host-only check that mx_gemm takes these formats and K; raises MoeError. (A
     call of no tokens: it checks them, reads nothing and launches nothing.)"""
+    if N > _I32_MAX or K > _I32_MAX:
+        raise MoeError(f"mx_gemm: N={N} or K={K} is too large")
     _check(lib().mx_gemm(None, None, a_fmt, None, None, w_fmt, 0, N, K, None, N, MOE_BF16, None), "mx_gemm")
 
 
