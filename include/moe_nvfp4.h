@@ -56,6 +56,7 @@ extern "C" {
 #define MOE_MAX_EXPERTS 1024  /* E and E_local */
 #define MOE_MAX_TOPK 32
 #define MOE_MAX_HIDDEN 16384  /* H, and I in moe_experts_fwd */
+#define MOE_MAX_GROUPED 32768 /* N and D of moe_grouped_gemm */
 
 int moe_abi_version(void);
 const char* moe_last_error(void);
@@ -608,6 +609,46 @@ int moe_combine_bwd(const void* d_out, int64_t d_out_row_stride, const void* row
                     const int32_t* exp2perm, const int32_t* perm2tok, const int32_t* total_rows,
                     const float* topk_weights, int T, int K, int64_t rows_max, int H, void* d_rows,
                     int64_t d_rows_stride, float* d_weights, void* stream);
+
+/* ------------------------------------------------------------------ products by expert
+ * The products of a caller's own experts on rows sorted by moe_dispatch, and
+ * their gradients (beside moe_experts_fwd_bf16, which keeps nothing for a
+ * backward pass), bf16 operands, fp32 accumulators. Expert e's rows are
+ *   r in [expert_offsets[e], expert_offsets[e] + expert_counts[e])
+ *   expert_offsets  device int32 [E + 1], ascending, the last at most rows_max
+ *   expert_counts   device int32 [E], each at most the distance to the next
+ *                   offset: the fields of those names in moe_route's metadata
+ *                   (any offsets will do, not multiples of a tile alone)
+ * Rows between an expert's last and the next offset (padding) are not read, and
+ * are written as zeros where rows are written; rows from the last offset on are
+ * neither read nor written. Maps that break these bounds give wrong rows, and
+ * never an access outside the rows.
+ * w device bf16 [E, N, D], contiguous. N and D multiples of 8 up to
+ * MOE_MAX_GROUPED; row strides of bf16 operands multiples of 8, at most 2^21.
+ * Every sum has a fixed order: results do not change from call to call. One
+ * launch each, no workspace.
+ *
+ * moe_grouped_gemm: out[r, n] = sum_d x[r, d] * w[e, n, d], rounded once.
+ *   x    device bf16 [rows_max, D];  out device [rows_max, N], out_dtype MOE_BF16 or
+ *        MOE_F32, row stride >= N */
+int moe_grouped_gemm(const uint16_t* x, int64_t x_row_stride, const uint16_t* w, const int32_t* expert_offsets,
+                     const int32_t* expert_counts, int64_t rows_max, int E, int N, int D, void* out,
+                     int64_t out_row_stride, int out_dtype, void* stream);
+
+/* Its input's gradient: d_x[r, d] = sum_n d_out[r, n] * w[e, n, d], rounded once.
+ *   d_out device bf16 [rows_max, N];  d_x device [rows_max, D], MOE_BF16 or MOE_F32 */
+int moe_grouped_gemm_dgrad(const uint16_t* d_out, int64_t d_out_row_stride, const uint16_t* w,
+                           const int32_t* expert_offsets, const int32_t* expert_counts, int64_t rows_max, int E, int N,
+                           int D, void* d_x, int64_t d_x_row_stride, int d_x_dtype, void* stream);
+
+/* Its weight's gradient: d_w[e, n, d] = sum_r d_out[r, n] * x[r, d] over e's rows
+ * (zeros for an expert without), rounded once; with `accumulate` nonzero added
+ * to what d_w holds, in fp32, and rounded once.
+ *   d_w  device [E, N, D], contiguous, MOE_BF16 or MOE_F32
+ * With rows_max 0 (and no accumulate) d_w is zeros. */
+int moe_grouped_gemm_wgrad(const uint16_t* d_out, int64_t d_out_row_stride, const uint16_t* x, int64_t x_row_stride,
+                           const int32_t* expert_offsets, const int32_t* expert_counts, int64_t rows_max, int E, int N,
+                           int D, int accumulate, void* d_w, int d_w_dtype, void* stream);
 
 #ifdef __cplusplus
 }

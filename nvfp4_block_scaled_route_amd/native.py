@@ -25,7 +25,8 @@ EXPORTS = ("moe_abi_version", "moe_last_error", "moe_rows_max", "moe_meta_layout
            "moe_router_route", "moe_experts_fwd_w4a16", "moe_experts_fwd_bf16",
            "moe_validate_weights", "moe_workspace_bytes", "moe_experts_fwd_noalloc",
            "moe_experts_finalize", "mx_quant", "mx_dequant", "mx_add_norm_quant", "mx_gemm",
-           "moe_dispatch", "moe_dispatch_bwd", "moe_combine", "moe_combine_bwd")
+           "moe_dispatch", "moe_dispatch_bwd", "moe_combine", "moe_combine_bwd",
+           "moe_grouped_gemm", "moe_grouped_gemm_dgrad", "moe_grouped_gemm_wgrad")
 
 
 class MoeMetaLayout(ctypes.Structure):
@@ -101,6 +102,9 @@ def lib() -> ctypes.CDLL:
         "moe_dispatch_bwd": (i32, [vp, i64, i32, vp, i32, i32, i64, i32, vp, i64, vp]),
         "moe_combine": (i32, [vp, i64, i32, vp, vp, i32, i32, i64, i32, vp, i64, vp]),
         "moe_combine_bwd": (i32, [vp, i64, vp, i64, i32, vp, vp, vp, vp, i32, i32, i64, i32, vp, i64, vp, vp]),
+        "moe_grouped_gemm": (i32, [vp, i64, vp, vp, vp, i64, i32, i32, i32, vp, i64, i32, vp]),
+        "moe_grouped_gemm_dgrad": (i32, [vp, i64, vp, vp, vp, i64, i32, i32, i32, vp, i64, i32, vp]),
+        "moe_grouped_gemm_wgrad": (i32, [vp, i64, vp, i64, vp, vp, i64, i32, i32, i32, i32, vp, i32, vp]),
         "moe_validate_weights": (i32, [ctypes.POINTER(MoeNvfp4Weights), i32, i32, i32, i32]),
         "moe_workspace_bytes": (i64, [i32, i32, i32, i32, i32, i32, i32, ctypes.POINTER(MoeWorkspaceLayout)]),
     }
@@ -538,5 +542,60 @@ def moe_combine_bwd(d_out, rows, exp2perm, perm2tok, total_rows, topk_weights, d
                                _flat(call, "total_rows", total_rows, _I32, (1,), dev),
                                _flat(call, "topk_weights", topk_weights, _F32, maps, dev), T, K, R, H,
                                d_rows.data_ptr(), ld_d, _flat(call, "d_weights", d_weights, _F32, maps, dev), st)
+    if rc:
+        _check(rc, call)
+
+
+# ------------------------------------------------------------------ products by expert
+def _experts_shape(call, name, t):
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{call}: {name} must be a tensor of three dimensions")
+    shape = t.shape
+    if max(shape) > _I32_MAX:
+        raise MoeError(f"{call}: {name} of shape {tuple(shape)} is too large")
+    return shape
+
+
+def _grouped(call, fn, x, w, expert_offsets, expert_counts, out, stream, grad) -> None:
+    E, N, D = _experts_shape(call, "w", w)
+    R = _shape2(call, "x" if not grad else "d_out", x)[0]
+    dev, st = _where(call, x, stream)
+    cols_in, cols_out = (N, D) if grad else (D, N)
+    ld_x = _rows(call, "d_out" if grad else "x", x, _BF16_TYPES, (R, cols_in), dev)
+    ld_o = _rows(call, "d_x" if grad else "out", out, _TYPED_ROWS, (R, cols_out), dev)
+    rc = fn(x.data_ptr(), ld_x, _flat(call, "w", w, _BF16_TYPES, (E, N, D), dev),
+            _flat(call, "expert_offsets", expert_offsets, _I32, (E + 1,), dev),
+            _flat(call, "expert_counts", expert_counts, _I32, (E,), dev), R, E, N, D, out.data_ptr(), ld_o,
+            MOE_F32 if out.dtype == torch.float32 else MOE_BF16, st)
+    if rc:
+        _check(rc, call)
+
+
+def moe_grouped_gemm(x, w, expert_offsets, expert_counts, out, stream=None) -> None:
+    """out[r] = w[e] x[r] over the rows of each expert e: x bf16 [R, D], w bf16
+    [E, N, D], out bf16 or fp32 [R, N]; padding rows of an expert become zeros."""
+    _grouped("moe_grouped_gemm", lib().moe_grouped_gemm, x, w, expert_offsets, expert_counts, out, stream, False)
+
+
+def moe_grouped_gemm_dgrad(d_out, w, expert_offsets, expert_counts, d_x, stream=None) -> None:
+    """moe_grouped_gemm's input gradient: d_x[r] = w[e] transposed times d_out[r]."""
+    _grouped("moe_grouped_gemm_dgrad", lib().moe_grouped_gemm_dgrad, d_out, w, expert_offsets, expert_counts, d_x, stream,
+             True)
+
+
+def moe_grouped_gemm_wgrad(d_out, x, expert_offsets, expert_counts, d_w, accumulate=False, stream=None) -> None:
+    """moe_grouped_gemm's weight gradient: d_w[e] = (or, with accumulate, +=) the
+    sum over e's rows of d_out[r] x[r]; d_w bf16 or fp32 [E, N, D]."""
+    call = "moe_grouped_gemm_wgrad"
+    shape = E, N, D = _experts_shape(call, "d_w", d_w)
+    R = _shape2(call, "x", x)[0]
+    dev, st = _where(call, d_w, stream)
+    ld_o = _rows(call, "d_out", d_out, _BF16_TYPES, (R, N), dev)
+    ld_x = _rows(call, "x", x, _BF16_TYPES, (R, D), dev)
+    rc = lib().moe_grouped_gemm_wgrad(d_out.data_ptr(), ld_o, x.data_ptr(), ld_x,
+                                      _flat(call, "expert_offsets", expert_offsets, _I32, (E + 1,), dev),
+                                      _flat(call, "expert_counts", expert_counts, _I32, (E,), dev), R, E, N, D,
+                                      1 if accumulate else 0, _flat(call, "d_w", d_w, _TYPED_ROWS, shape, dev),
+                                      MOE_F32 if d_w.dtype == torch.float32 else MOE_BF16, st)
     if rc:
         _check(rc, call)
