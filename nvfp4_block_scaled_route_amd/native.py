@@ -26,7 +26,8 @@ EXPORTS = ("moe_abi_version", "moe_last_error", "moe_rows_max", "moe_meta_layout
            "moe_validate_weights", "moe_workspace_bytes", "moe_experts_fwd_noalloc",
            "moe_experts_finalize", "mx_quant", "mx_dequant", "mx_add_norm_quant", "mx_gemm",
            "moe_dispatch", "moe_dispatch_bwd", "moe_combine", "moe_combine_bwd",
-           "moe_grouped_gemm", "moe_grouped_gemm_dgrad", "moe_grouped_gemm_wgrad")
+           "moe_grouped_gemm", "moe_grouped_gemm_dgrad", "moe_grouped_gemm_wgrad", "moe_swiglu", "moe_swiglu_bwd",
+           "fp8_quant", "fp8_quant_weight", "fp8_gemm")
 
 
 class MoeMetaLayout(ctypes.Structure):
@@ -105,6 +106,11 @@ def lib() -> ctypes.CDLL:
         "moe_grouped_gemm": (i32, [vp, i64, vp, vp, vp, i64, i32, i32, i32, vp, i64, i32, vp]),
         "moe_grouped_gemm_dgrad": (i32, [vp, i64, vp, vp, vp, i64, i32, i32, i32, vp, i64, i32, vp]),
         "moe_grouped_gemm_wgrad": (i32, [vp, i64, vp, i64, vp, vp, i64, i32, i32, i32, i32, vp, i32, vp]),
+        "moe_swiglu": (i32, [vp, i64, i32, vp, vp, i64, i32, vp, i64, vp]),
+        "moe_swiglu_bwd": (i32, [vp, i64, vp, i64, i32, vp, vp, i64, i32, vp, i64, vp]),
+        "fp8_quant": (i32, [vp, i64, i32, i32, vp, vp, i64, vp]),
+        "fp8_quant_weight": (i32, [vp, i64, i32, i32, vp, vp, vp, i64, vp, vp]),
+        "fp8_gemm": (i32, [vp, vp, i64, vp, i64, vp, i32, i32, i32, vp, i64, vp]),
         "moe_validate_weights": (i32, [ctypes.POINTER(MoeNvfp4Weights), i32, i32, i32, i32]),
         "moe_workspace_bytes": (i64, [i32, i32, i32, i32, i32, i32, i32, ctypes.POINTER(MoeWorkspaceLayout)]),
     }
@@ -597,5 +603,91 @@ def moe_grouped_gemm_wgrad(d_out, x, expert_offsets, expert_counts, d_w, accumul
                                       _flat(call, "expert_counts", expert_counts, _I32, (E,), dev), R, E, N, D,
                                       1 if accumulate else 0, _flat(call, "d_w", d_w, _TYPED_ROWS, shape, dev),
                                       MOE_F32 if d_w.dtype == torch.float32 else MOE_BF16, st)
+    if rc:
+        _check(rc, call)
+
+
+def moe_swiglu(gate_up, perm2tok, total_rows, inter, stream=None) -> None:
+    """inter[r] = silu(gate_up[r, :I]) * gate_up[r, I:] on the rows that hold a token;
+    padding rows below total_rows become zeros. gate_up [R, 2 I] and inter [R, I] of
+    one type, bf16 or fp32."""
+    call = "moe_swiglu"
+    shape = R, I = _shape2(call, "inter", inter)
+    dtype, types = _row_type(call, inter), (inter.dtype,)
+    dev, st = _where(call, inter, stream)
+    ld_g = _rows(call, "gate_up", gate_up, types, (R, 2 * I), dev)
+    ld_i = _rows(call, "inter", inter, types, shape, dev)
+    rc = lib().moe_swiglu(gate_up.data_ptr(), ld_g, dtype, _flat(call, "perm2tok", perm2tok, _I32, (R,), dev),
+                          _flat(call, "total_rows", total_rows, _I32, (1,), dev), R, I, inter.data_ptr(), ld_i, st)
+    if rc:
+        _check(rc, call)
+
+
+def moe_swiglu_bwd(d_inter, gate_up, perm2tok, total_rows, d_gate_up, stream=None) -> None:
+    """moe_swiglu's gradient with respect to gate_up, from gate_up itself; d_gate_up may
+    be gate_up."""
+    call = "moe_swiglu_bwd"
+    shape = R, I = _shape2(call, "d_inter", d_inter)
+    dtype, types = _row_type(call, d_inter), (d_inter.dtype,)
+    dev, st = _where(call, d_inter, stream)
+    ld_i = _rows(call, "d_inter", d_inter, types, shape, dev)
+    ld_g = _rows(call, "gate_up", gate_up, types, (R, 2 * I), dev)
+    ld_d = _rows(call, "d_gate_up", d_gate_up, types, (R, 2 * I), dev)
+    rc = lib().moe_swiglu_bwd(d_inter.data_ptr(), ld_i, gate_up.data_ptr(), ld_g, dtype,
+                              _flat(call, "perm2tok", perm2tok, _I32, (R,), dev),
+                              _flat(call, "total_rows", total_rows, _I32, (1,), dev), R, I, d_gate_up.data_ptr(), ld_d, st)
+    if rc:
+        _check(rc, call)
+
+
+# ------------------------------------------------------------------ 8-bit products
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def fp8_quant(x, codes, sf, stream=None) -> None:
+    """bf16 x [T, H] -> e4m3 codes [T, H] and fp32 scales [ceil(H/128), T], one for
+    128 values of a row (sf's rows may be longer than T)."""
+    call = "fp8_quant"
+    shape = T, H = _shape2(call, "x", x)
+    dev, st = _where(call, x, stream)
+    ld = _rows(call, "x", x, _BF16_TYPES, shape, dev)
+    ld_s = _rows(call, "sf", sf, _F32, (_blocks(H), T), dev)
+    rc = lib().fp8_quant(x.data_ptr(), ld, T, H, _flat(call, "codes", codes, _E4M3_TYPES, shape, dev), sf.data_ptr(), ld_s, st)
+    if rc:
+        _check(rc, call)
+
+
+def fp8_quant_weight(w, codes, sf, codes_t=None, sf_t=None, stream=None) -> None:
+    """bf16 w [N, K] -> e4m3 codes [N, K] and fp32 scales [ceil(N/128), ceil(K/128)], one
+    for 128 x 128 values; and the same transposed into codes_t [K, N] and sf_t."""
+    call = "fp8_quant_weight"
+    shape = N, K = _shape2(call, "w", w)
+    dev, st = _where(call, w, stream)
+    ld = _rows(call, "w", w, _BF16_TYPES, shape, dev)
+    ld_t, ct, stt = 0, None, None
+    if codes_t is not None:
+        ld_t, ct = _rows(call, "codes_t", codes_t, _E4M3_TYPES, (K, N), dev), codes_t.data_ptr()
+    if sf_t is not None:
+        stt = _flat(call, "sf_t", sf_t, _F32, (_blocks(K), _blocks(N)), dev)
+    rc = lib().fp8_quant_weight(w.data_ptr(), ld, N, K, _flat(call, "codes", codes, _E4M3_TYPES, shape, dev),
+                                _flat(call, "sf", sf, _F32, (_blocks(N), _blocks(K)), dev), ct, ld_t, stt, st)
+    if rc:
+        _check(rc, call)
+
+
+def fp8_gemm(a_codes, a_sf, w_codes, w_sf, out, stream=None) -> None:
+    """out bf16 [T, N] = a [T, K] times w [N, K] transposed: e4m3 codes, a_sf as fp8_quant
+    writes it, w_sf one scale for 128 x 128."""
+    call = "fp8_gemm"
+    shape = T, N = _shape2(call, "out", out)
+    K = _shape2(call, "w_codes", w_codes)[1]
+    dev, st = _where(call, out, stream)
+    ld = _rows(call, "out", out, _BF16_TYPES, shape, dev)
+    a = _flat(call, "a_codes", a_codes, _E4M3_TYPES, (T, K), dev)
+    ld_s = _rows(call, "a_sf", a_sf, _F32, (_blocks(K), T), dev)
+    ld_w = _rows(call, "w_codes", w_codes, _E4M3_TYPES, (N, K), dev)
+    rc = lib().fp8_gemm(a, a_sf.data_ptr(), ld_s, w_codes.data_ptr(), ld_w,
+                        _flat(call, "w_sf", w_sf, _F32, (_blocks(N), _blocks(K)), dev), T, N, K, out.data_ptr(), ld, st)
     if rc:
         _check(rc, call)
