@@ -29,6 +29,7 @@ struct GgArgs {
     const int32_t* counts;
     int E;
     int64_t R;
+    int row_blocks;         // blocks of rows there are at most
     int M, N, K;            // output rows (weight gradient), output columns, contraction (else: the expert's rows)
     uint8_t* out;
     int64_t out_stride, out_group;          // bytes
@@ -38,18 +39,25 @@ struct GgArgs {
 constexpr int kGgElems = 64;        // contraction of a stage: 128 bytes of a row, a whole cache line
 constexpr uint32_t kOutside = 0x80000000u;      // an offset past the descriptors' range: zeros arrive
 
+// A descriptor in scalar registers, which the copies take it from, whatever the compiler keeps its address in.
+__device__ __forceinline__ u32x4 gg_desc(const uint8_t* base) {
+    const uint64_t p = reinterpret_cast<uint64_t>(base);
+    return buffer_desc(reinterpret_cast<const void*>(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(p >> 32)) << 32) |
+                                                     (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)p)));
+}
+
 // An operand whose rows hold the contraction: ROWS rows x 64 elements in LDS,
 // the 8 chunks of a row permuted so that 16 consecutive rows' reads of one chunk
 // spread over all banks.
 template <int ROWS>
 struct Along {
     static constexpr int kCopies = ROWS * 128 / 4096, kSize = ROWS * 128;
-    u32x4 rsrc;
+    const uint8_t* base;
     uint32_t off[kCopies];
     int chunk, k_bytes;
     __device__ __forceinline__ static int swizzle(int chunk, int row) { return chunk ^ (row & 7) ^ ((row >> 3) & 1); }
-    __device__ __forceinline__ void init(const uint8_t* base, int64_t stride, int rows, int k, int wave, int lane) {
-        rsrc = buffer_desc(base);
+    __device__ __forceinline__ void init(const uint8_t* b, int64_t stride, int rows, int k, int wave, int lane) {
+        base = b;
         const int r0 = 8 * wave + lane / 8;
         chunk = swizzle(lane % 8, r0);          // rows 32 apart have the same
         k_bytes = 2 * k;
@@ -57,8 +65,8 @@ struct Along {
         for (int q = 0; q < kCopies; ++q) off[q] = r0 + 32 * q < rows ? (uint32_t)((r0 + 32 * q) * stride + chunk * 16) : kOutside;
     }
     __device__ __forceinline__ void issue(uint32_t lds, int s, int q, int wave) const {
-        lds_copy16(rsrc, __builtin_amdgcn_readfirstlane(lds + (4 * q + wave) * 1024),
-                   s * 128 + chunk * 16 < k_bytes ? off[q] : kOutside, (uint32_t)(s * 128));
+        lds_copy16(gg_desc(base), __builtin_amdgcn_readfirstlane(lds + (4 * q + wave) * 1024),
+                   s * 128 + chunk * 16 < k_bytes ? off[q] : kOutside, (uint32_t)__builtin_amdgcn_readfirstlane(s * 128));
     }
     // 8 elements of the contraction of row `row`: group g's of a step
     __device__ __forceinline__ static bf16x8 read(const uint8_t* at, int tile, int step, int lane) {
@@ -90,7 +98,7 @@ struct Across {
         for (int q = 0; q < kCopies; ++q) off[q] = chunk * 8 < cols ? (uint32_t)((row + 4 * kRowsPer * q) * stride + chunk * 16) : kOutside;
     }
     __device__ __forceinline__ void issue(uint32_t lds, int s, int q, int wave) const {
-        lds_copy16(buffer_desc(base + s * stage), __builtin_amdgcn_readfirstlane(lds + (4 * q + wave) * 1024),
+        lds_copy16(gg_desc(base + s * stage), __builtin_amdgcn_readfirstlane(lds + (4 * q + wave) * 1024),
                    s * kGgElems + row + 4 * kRowsPer * q < k ? off[q] : kOutside, 0u);
     }
     __device__ __forceinline__ static bf16x8 read(const uint8_t* at, int tile, int step, int lane) {
@@ -104,19 +112,22 @@ struct Across {
     }
 };
 
-// ------------------------------------------------------------------ rows to workgroups
-// An expert's rows as a workgroup needs them.
-struct GgGroup {
-    int e, first, rows, end;        // first row, rows with tokens, the end of its padding rows
-    int tile, tiles;                // the block of the output among the expert's, its blocks of rows
+// ------------------------------------------------------------------ experts' rows
+// What the maps hold of expert e: whatever that is, its rows stay inside [0, R).
+__device__ __forceinline__ int gg_clamp(int v, int low, int high) { return v < low ? low : v < high ? v : high; }
+
+// A block of the output and what it is computed from.
+struct GgBlock {
+    int e, row, rows, end;  // expert, its first row, its rows, the end of its padding rows
+    int tile, tiles;        // the block among the expert's, the expert's blocks of rows
 };
 
-__device__ __forceinline__ void gg_rows(const GgArgs& a, int e, int& first, int& rows, int& end) {
-    // whatever the maps hold, rows stay inside [0, R) and an expert's inside its own
-    const int R = (int)a.R, f = a.offsets[e], n = a.offsets[e + 1], c = a.counts[e];
-    first = f < 0 ? 0 : f < R ? f : R;
-    end = n < first ? first : n < R ? n : R;
-    rows = c < 0 ? 0 : c < end - first ? c : end - first;
+__device__ __forceinline__ void gg_rows(const GgArgs& a, int e, GgBlock& b) {
+    const int R = (int)a.R;
+    b.e = e;
+    b.row = gg_clamp(a.offsets[e], 0, R);
+    b.end = gg_clamp(a.offsets[e + 1], b.row, R);
+    b.rows = gg_clamp(a.counts[e], 0, b.end - b.row);
 }
 
 // XCD x (workgroups are dealt to the 8 round robin) gets a contiguous run of
@@ -127,180 +138,188 @@ __device__ __forceinline__ int xcd_run(int total) {
 }
 
 // The expert and block of this workgroup: experts in order, each with
-// ceil(its rows / bm) x nt blocks. Every thread counts a few experts' blocks.
-__device__ __forceinline__ bool gg_find(const GgArgs& a, int bm, int nt, GgGroup& out) {
+// ceil(its rows / bm) x nt blocks, padding rows among them. Every thread counts a
+// few experts' blocks; at most `most` blocks of rows in all (more only where the
+// maps are wrong).
+__device__ __forceinline__ bool gg_find(const GgArgs& a, int bm, int nt, GgBlock& out) {
     __shared__ int s_sum[4];
-    __shared__ GgGroup s_out;
+    __shared__ GgBlock s_out;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int per = (a.E + 255) / 256, e0 = tid * per;
     int mine = 0;
-    for (int i = 0; i < per; ++i) {
-        if (e0 + i >= a.E) break;
-        int first, rows, end;
-        gg_rows(a, e0 + i, first, rows, end);
-        mine += (end - first + bm - 1) / bm;
+    for (int e = e0; e < e0 + per && e < a.E; ++e) {
+        GgBlock g;
+        gg_rows(a, e, g);
+        mine += (g.end - g.row + bm - 1) / bm;
     }
     const int upto = wave_inclusive_scan(mine);
     if (lane == 63) s_sum[wave] = upto;
     if (tid == 0) s_out.e = -1;
     __syncthreads();
-    int before = upto - mine;
+    int before = upto - mine, total = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
     for (int w = 0; w < wave; ++w) before += s_sum[w];
-    const int total = (s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3]) * nt;
-    const int id = xcd_run(total);
+    total = total < a.row_blocks ? total : a.row_blocks;
+    const int id = xcd_run(total * nt), block = id / nt;
     if (id < 0) return false;
-    if (id >= before * nt && id < (before + mine) * nt) {
-        for (int i = 0; i < per; ++i) {
-            if (e0 + i >= a.E) break;
-            GgGroup g;
-            g.e = e0 + i;
-            gg_rows(a, g.e, g.first, g.rows, g.end);
-            g.tiles = (g.end - g.first + bm - 1) / bm;
+    if (block >= before && block < before + mine) {
+        for (int e = e0; e < e0 + per && e < a.E; ++e) {
+            GgBlock g;
+            gg_rows(a, e, g);
+            g.tiles = (g.end - g.row + bm - 1) / bm;
             g.tile = id - before * nt;
-            if (g.tile >= 0 && g.tile < g.tiles * nt) s_out = g;
+            if (block >= before && block < before + g.tiles) s_out = g;
             before += g.tiles;
         }
     }
     __syncthreads();
     out.e = __builtin_amdgcn_readfirstlane(s_out.e);
-    if (out.e < 0) return false;
-    out.first = __builtin_amdgcn_readfirstlane(s_out.first);
+    out.row = __builtin_amdgcn_readfirstlane(s_out.row);
     out.rows = __builtin_amdgcn_readfirstlane(s_out.rows);
     out.end = __builtin_amdgcn_readfirstlane(s_out.end);
     out.tile = __builtin_amdgcn_readfirstlane(s_out.tile);
     out.tiles = __builtin_amdgcn_readfirstlane(s_out.tiles);
-    return true;
+    return out.e >= 0;
 }
 
 // ------------------------------------------------------------------ output
-template <int NW, bool F32>
-constexpr int gg_row_bytes() { return 32 * NW * (F32 ? 4 : 2) + 16; }
+// 32 rows x NT tiles of 32 columns of a wave's block, turned in the wave's own part
+// of the LDS: a lane holds 4 consecutive columns of one row at a time, and whole
+// 16-byte pieces of the rows are stored. Of `left` rows, those from `live` on are
+// zeros. ADD: added to what the output holds, in fp32, rounded once.
+template <int NT, bool F32>
+constexpr int gg_row_bytes() { return 32 * NT * (F32 ? 4 : 2) + 16; }
 
-// 32 rows of a wave's block: a lane holds 4 consecutive columns of one row at a
-// time; the wave turns its NW tiles through its own part of the LDS and stores
-// whole 16-byte pieces. Of `left` rows, those from `live` on are zeros.
-template <int NW, bool F32, bool ADD>
-__device__ __forceinline__ void gg_store(uint8_t* out, int64_t stride, bool vec, uint8_t* slab, const gg_f16v (&acc)[NW],
+template <int NT, bool F32, bool ADD>
+__device__ __forceinline__ void gg_store(uint8_t* out, int64_t stride, bool vec, uint8_t* slab, const gg_f16v (&acc)[NT],
                                          int live, int left, int cols, int lane) {
-    constexpr int kRow = gg_row_bytes<NW, F32>(), kEs = F32 ? 4 : 2, kPiece = 16 / kEs, kPieces = 32 * NW / kPiece;
+    constexpr bool kWide = F32 || ADD;      // fp32 in LDS
+    constexpr int kRow = gg_row_bytes<NT, kWide>(), kEs = F32 ? 4 : 2, kPiece = 16 / kEs, kPieces = 32 * NT / kPiece;
+    constexpr int kRowsPer = 64 / kPieces, kCount = 32 / kRowsPer;
     const int r = lane & 31, g = lane >> 5;
+    const bool zero = r >= live;
     wave_lds_sync();
 #pragma unroll
-    for (int n = 0; n < NW; ++n)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const int c = 32 * n + 8 * q + 4 * g;
-            floatx4 v = {acc[n][4 * q], acc[n][4 * q + 1], acc[n][4 * q + 2], acc[n][4 * q + 3]};
-            if (r >= live) v = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-            if constexpr (F32 || ADD) *reinterpret_cast<floatx4*>(slab + r * kRow + c * 4) = v;
-            else *reinterpret_cast<uint2*>(slab + r * kRow + c * 2) = make_uint2(f32_to_bf16(v[0]) | (f32_to_bf16(v[1]) << 16),
-                                                                                 f32_to_bf16(v[2]) | (f32_to_bf16(v[3]) << 16));
+            const gg_f16v& a = acc[n];
+            const float v0 = zero ? 0.0f : a[4 * q], v1 = zero ? 0.0f : a[4 * q + 1];
+            const float v2 = zero ? 0.0f : a[4 * q + 2], v3 = zero ? 0.0f : a[4 * q + 3];
+            if constexpr (kWide) *reinterpret_cast<floatx4*>(slab + r * kRow + c * 4) = floatx4{v0, v1, v2, v3};
+            else *reinterpret_cast<uint2*>(slab + r * kRow + c * 2) = make_uint2(bf16x2_pack(v0, v1), bf16x2_pack(v2, v3));
         }
     wave_lds_sync();
-#pragma unroll 4
-    for (int j = 0; j < 32 * kPieces / 64; ++j) {
-        const int i = lane + 64 * j, row = i / kPieces, c = (i % kPieces) * kPiece;
-        if (row >= left || c >= cols) continue;
-        uint8_t* dst = out + row * stride + c * kEs;
-        const uint8_t* src = slab + row * kRow + c * kEs;
-        if (vec && c + kPiece <= cols) {
-            *reinterpret_cast<u32x4*>(dst) = *reinterpret_cast<const u32x4*>(src);
+    const int row = lane / kPieces, c = lane % kPieces * kPiece;
+    const uint8_t* src = slab + row * kRow + c * (kWide ? 4 : 2);
+    uint8_t* dst = out + row * stride + c * kEs;
+    // a piece of the output: what LDS holds, or that and the output's own
+    const auto piece = [](const uint8_t* p, u32x4 old) {
+        if constexpr (!ADD) {
+            return *reinterpret_cast<const u32x4*>(p);
+        } else if constexpr (F32) {
+            const floatx4 v = *reinterpret_cast<const floatx4*>(p);
+            return u32x4{__float_as_uint(__fadd_rn(v[0], __uint_as_float(old[0]))), __float_as_uint(__fadd_rn(v[1], __uint_as_float(old[1]))),
+                         __float_as_uint(__fadd_rn(v[2], __uint_as_float(old[2]))), __float_as_uint(__fadd_rn(v[3], __uint_as_float(old[3])))};
         } else {
+            u32x4 o;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float lo = reinterpret_cast<const float*>(p)[2 * i], hi = reinterpret_cast<const float*>(p)[2 * i + 1];
+                o[i] = bf16x2_pack(__fadd_rn(lo, bf16_to_f32(old[i] & 0xFFFFu)), __fadd_rn(hi, __uint_as_float(old[i] & 0xFFFF0000u)));
+            }
+            return o;
+        }
+    };
+    if (vec && left >= 32 && cols >= 32 * NT) {
+        constexpr int kBatch = kCount < 8 ? kCount : 8;
+#pragma unroll
+        for (int j0 = 0; j0 < kCount; j0 += kBatch) {
+            u32x4 v[kBatch] = {};
+            if constexpr (ADD) {
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) v[j] = *reinterpret_cast<const u32x4*>(dst + (j0 + j) * kRowsPer * stride);
+            }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) v[j] = piece(src + (j0 + j) * kRowsPer * kRow, v[j]);
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) __builtin_nontemporal_store(v[j], reinterpret_cast<u32x4*>(dst + (j0 + j) * kRowsPer * stride));
+        }
+        return;
+    }
+    for (int j = 0; j < kCount; ++j, src += kRowsPer * kRow, dst += kRowsPer * stride) {
+        if (row + j * kRowsPer >= left || c >= cols) continue;
+        if (vec && c + kPiece <= cols) {
+            u32x4 old = {};
+            if constexpr (ADD) old = *reinterpret_cast<const u32x4*>(dst);
+            *reinterpret_cast<u32x4*>(dst) = piece(src, old);
+        } else {        // (accumulating outputs are contiguous, their rows whole pieces but for a bf16 row's or fp32 row's own end)
             for (int k = 0; k < kPiece && c + k < cols; ++k) {
-                if constexpr (F32) reinterpret_cast<float*>(dst)[k] = reinterpret_cast<const float*>(src)[k];
-                else reinterpret_cast<uint16_t*>(dst)[k] = reinterpret_cast<const uint16_t*>(src)[k];
+                float v = kWide ? reinterpret_cast<const float*>(src)[k] : 0.0f;
+                if constexpr (F32) {
+                    float* d = reinterpret_cast<float*>(dst) + k;
+                    *d = ADD ? __fadd_rn(v, *d) : v;
+                } else if constexpr (ADD) {
+                    uint16_t* d = reinterpret_cast<uint16_t*>(dst) + k;
+                    *d = (uint16_t)f32_to_bf16(__fadd_rn(v, bf16_to_f32(*d)));
+                } else {
+                    reinterpret_cast<uint16_t*>(dst)[k] = reinterpret_cast<const uint16_t*>(src)[k];
+                }
             }
         }
     }
 }
 
-// The same for a sum onto what the output holds (bf16: added in fp32, rounded once).
-template <int NW, bool F32>
-__device__ __forceinline__ void gg_add(uint8_t* out, int64_t stride, uint8_t* slab, const gg_f16v (&acc)[NW], int left, int cols,
-                                       int lane) {
-    constexpr int kRow = gg_row_bytes<NW, true>();
-    const int r = lane & 31, g = lane >> 5;
-    wave_lds_sync();
-#pragma unroll
-    for (int n = 0; n < NW; ++n)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<floatx4*>(slab + r * kRow + (32 * n + 8 * q + 4 * g) * 4) =
-                floatx4{acc[n][4 * q], acc[n][4 * q + 1], acc[n][4 * q + 2], acc[n][4 * q + 3]};
-    wave_lds_sync();
-#pragma unroll 8
-    for (int j = 0; j < 32 * NW / 2; ++j) {
-        const int i = lane + 64 * j, row = i / (32 * NW), c = i % (32 * NW);
-        if (row >= left || c >= cols) continue;
-        const float v = *reinterpret_cast<const float*>(slab + row * kRow + c * 4);
-        if constexpr (F32) {
-            float* dst = reinterpret_cast<float*>(out + row * stride) + c;
-            *dst = __fadd_rn(*dst, v);
-        } else {
-            uint16_t* dst = reinterpret_cast<uint16_t*>(out + row * stride) + c;
-            *dst = (uint16_t)f32_to_bf16(__fadd_rn(bf16_to_f32(*dst), v));
-        }
-    }
-}
-
 // ------------------------------------------------------------------ the kernel
-// 4 waves, WM along the output's rows; a wave has MW x NW tiles of 32 x 32.
+// 4 waves, WM along the output's rows; a wave has MW x NW tiles of 32 x 32, its
+// tiles' rows dealt round the waves, so that a block of few rows is few tiles of
+// every wave's.
 enum GgKind { kGgRows, kGgRowsT, kGgWeight };       // forward, input gradient, weight gradient
 
-template <int KIND, int WM, int MW, int NW>
+template <int KIND, int WM, int MW, int NW, bool F32, bool ADD>
 struct GgShape {
     static constexpr int kWN = 4 / WM, kBM = 32 * WM * MW, kBN = 32 * kWN * NW;
     using A = std::conditional_t<KIND == kGgWeight, Across<kBM>, Along<kBM>>;
     using B = std::conditional_t<KIND == kGgRows, Along<kBN>, Across<kBN>>;
     static constexpr int kAll = A::kCopies + B::kCopies, kStage = A::kSize + B::kSize;
-    static constexpr int kPerCu = MW * NW >= 16 ? 1 : 2;
+    static constexpr int kSlab = 32 * gg_row_bytes<NW, F32 || ADD>();
+    static constexpr int kPerCu = MW * NW >= 16 || 4 * kStage > 160 * 1024 - 512 ? 1 : 2;
     static constexpr int kFit = (160 * 1024 / kPerCu - 256) / kStage, kRing = kFit < 6 ? kFit : 6;
-    static_assert(kRing >= 2 && (kRing - 1) * kAll < 64, "ring of stages");
+    static constexpr int kLds = kRing * kStage > 4 * kSlab ? kRing * kStage : 4 * kSlab;
+    static_assert(kRing >= 2 && kRing * kAll < 64, "ring of stages");
 };
 
 template <int KIND, int WM, int MW, int NW, bool F32, bool ADD>
-__global__ void __launch_bounds__(256, (GgShape<KIND, WM, MW, NW>::kPerCu)) grouped_gemm_kernel(GgArgs a) {
-    using S = GgShape<KIND, WM, MW, NW>;
-    constexpr int kOutRow = gg_row_bytes<NW, F32 || ADD>(), kAll = S::kAll;
-    constexpr int kLds = S::kRing * S::kStage > 4 * 32 * kOutRow ? S::kRing * S::kStage : 4 * 32 * kOutRow;
-    __shared__ __align__(16) uint8_t lds[kLds];
+__global__ void __launch_bounds__(256, (GgShape<KIND, WM, MW, NW, F32, ADD>::kPerCu)) grouped_gemm_kernel(GgArgs a) {
+    using S = GgShape<KIND, WM, MW, NW, F32, ADD>;
+    constexpr int kAll = S::kAll;
+    __shared__ __align__(16) uint8_t lds[S::kLds];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / S::kWN, wn = wave % S::kWN;
 
-    GgGroup g;
+    GgBlock b;
     const int nt = (a.N + S::kBN - 1) / S::kBN;
     if constexpr (KIND == kGgWeight) {
-        g.tiles = (a.M + S::kBM - 1) / S::kBM;
-        const int id = xcd_run(a.E * g.tiles * nt);
+        b.tiles = (a.M + S::kBM - 1) / S::kBM;
+        const int id = xcd_run(a.E * b.tiles * nt), e = id / (b.tiles * nt);
         if (id < 0) return;
-        g.e = id / (g.tiles * nt), g.tile = id - g.e * (g.tiles * nt);
-        gg_rows(a, g.e, g.first, g.rows, g.end);
+        gg_rows(a, e, b);
+        b.tile = id - e * (b.tiles * nt);
     } else {
-        if (!gg_find(a, S::kBM, nt, g)) return;
+        if (!gg_find(a, S::kBM, nt, b)) return;
     }
     // groups of 4 blocks of rows, column by column: what neighbours share stays in the XCD's L2
-    const int gm0 = g.tile / (4 * nt) * 4, gh = g.tiles - gm0 < 4 ? g.tiles - gm0 : 4, in = g.tile - gm0 * nt;
+    const int gm0 = b.tile / (4 * nt) * 4, gh = b.tiles - gm0 < 4 ? b.tiles - gm0 : 4, in = b.tile - gm0 * nt;
     const int m0 = (gm0 + in % gh) * S::kBM, n0 = (in / gh) * S::kBN;
+    // rows of the block that are computed, and that are written; contraction
+    const int live = KIND == kGgWeight ? a.M - m0 : b.rows - m0, left = KIND == kGgWeight ? live : b.end - b.row - m0;
+    const int k = KIND == kGgWeight ? b.rows : live > 0 ? a.K : 0, stages = (k + kGgElems - 1) / kGgElems;
+    if (ADD && k == 0) return;
 
     typename S::A ca;
     typename S::B cb;
-    int k, live, left;      // contraction; rows of the block that are computed, and that are written
-    if constexpr (KIND == kGgWeight) {
-        k = g.rows, live = left = a.M - m0;
-        ca.init(a.a + g.first * a.a_stride + 2 * (int64_t)m0, a.a_stride, a.M - m0, k, wave, lane);
-        cb.init(a.b + g.first * a.b_stride + 2 * (int64_t)n0, a.b_stride, a.N - n0, k, wave, lane);
-    } else {
-        live = g.rows - m0, left = g.end - g.first - m0;
-        k = live > 0 ? a.K : 0;
-        ca.init(a.a + (g.first + (int64_t)m0) * a.a_stride, a.a_stride, live, k, wave, lane);
-        const uint8_t* b = a.b + g.e * a.b_group;
-        if constexpr (KIND == kGgRows) cb.init(b + n0 * a.b_stride, a.b_stride, a.N - n0, k, wave, lane);
-        else cb.init(b + 2 * (int64_t)n0, a.b_stride, a.N - n0, k, wave, lane);
-    }
-    if (ADD && k == 0) return;
-    const int stages = (k + kGgElems - 1) / kGgElems;
     const uint32_t lds0 = lds_addr(lds);
-    auto copy = [&](int s, int q0, int q1) {
+    auto copy = [&](int s, int q0, int q1) __attribute__((always_inline)) {        // copies [q0, q1) of stage s
         const uint32_t at = lds0 + (s % S::kRing) * S::kStage;
 #pragma unroll
         for (int q = q0; q < q1; ++q) {
@@ -308,99 +327,142 @@ __global__ void __launch_bounds__(256, (GgShape<KIND, WM, MW, NW>::kPerCu)) grou
             else cb.issue(at + S::A::kSize, s, q - S::A::kCopies, wave);
         }
     };
+    if (stages > 0) {
+        if constexpr (KIND == kGgWeight) {
+            ca.init(a.a + b.row * a.a_stride + 2 * (int64_t)m0, a.a_stride, live, k, wave, lane);
+            cb.init(a.b + b.row * a.b_stride + 2 * (int64_t)n0, a.b_stride, a.N - n0, k, wave, lane);
+        } else {
+            const uint8_t* w = a.b + b.e * a.b_group;
+            ca.init(a.a + (b.row + (int64_t)m0) * a.a_stride, a.a_stride, live, k, wave, lane);
+            if constexpr (KIND == kGgRows) cb.init(w + n0 * a.b_stride, a.b_stride, a.N - n0, k, wave, lane);
+            else cb.init(w + 2 * (int64_t)n0, a.b_stride, a.N - n0, k, wave, lane);
+        }
+#pragma unroll
+        for (int s = 0; s < S::kRing; ++s) copy(s, 0, kAll);
+    }
     struct Operands {
         bf16x8 a[MW], b[NW];
     };
-    auto read = [&](int s, int step, Operands& o) {
-        const uint8_t* at = lds + (s % S::kRing) * S::kStage;
-#pragma unroll
-        for (int n = 0; n < NW; ++n) o.b[n] = S::B::read(at + S::A::kSize, wn * NW + n, step, lane);
-#pragma unroll
-        for (int m = 0; m < MW; ++m) o.a[m] = S::A::read(at, wm * MW + m, step, lane);
-    };
-    gg_f16v acc[MW][NW];
-#pragma unroll
-    for (int m = 0; m < MW; ++m)
-#pragma unroll
-        for (int n = 0; n < NW; ++n)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[m][n][i] = 0.0f;
-    auto mfma = [&](const Operands& o, int m) {
-#pragma unroll
-        for (int n = 0; n < NW; ++n) acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(o.b[n], o.a[m], acc[m][n], 0, 0, 0);
-    };
-    auto mfmas = [&](const Operands& o) {
-#pragma unroll
-        for (int m = 0; m < MW; ++m) mfma(o, m);
-        __builtin_amdgcn_sched_barrier(0);
-    };
+    constexpr int kSlots = MW * NW, kReads = 2 * (MW + NW), kFree = kSlots / 4, kCopySlots = 2 * kSlots - kFree;
 
-    // A ring of stages as in the MX product: one barrier a stage, in front of its
-    // last step's MFMAs; every wave holds what it still needs of the stage by
-    // then, and the copies of stage s + kRing go into its buffer behind it.
-    if (stages > 0) {
+    // The block, of which LIVE row tiles a wave or fewer hold rows.
+    //
+    // A ring of stages, a stage four steps of 16. Its operands are read in two
+    // bursts around its beginning, steps 0 and 1 during the last step of the stage
+    // before, 2 and 3 during its first: the buffer is free soon after (the first
+    // barrier; the copies of stage s + kRing go into it, spread over the MFMAs that
+    // follow), and the next one is not needed before the last step (the second
+    // barrier, in front of which every wave waits for its own copies). So a copy
+    // has half a stage more to arrive than the ring has stages.
+    auto compute = [&](auto tiles) __attribute__((always_inline)) {
+        constexpr int LIVE = decltype(tiles)::value;
+        gg_f16v acc[LIVE][NW];
 #pragma unroll
-        for (int s = 0; s < S::kRing; ++s) copy(s, 0, kAll);
-        Operands o0, o1;
-        __builtin_amdgcn_s_waitcnt(vmcnt_at_most((S::kRing - 1) * kAll));
-        __syncthreads();
-        read(0, 0, o0);
-        for (int s = 0; s < stages; ++s) {
-            read(s, 1, o1);
-            mfmas(o0);
-            read(s, 2, o0);
-            mfmas(o1);
-            read(s, 3, o1);
-            mfmas(o0);
-            __builtin_amdgcn_s_waitcnt(vmcnt_at_most((S::kRing - 2) * kAll) & lgkmcnt_zero());
+        for (int m = 0; m < LIVE; ++m)
+#pragma unroll
+            for (int n = 0; n < NW; ++n)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[m][n][i] = 0.0f;
+        if (stages > 0) {
+            Operands o0, o1, o2, o3;
+            auto read = [&](int s, int step, Operands& o, int i) __attribute__((always_inline)) {  // operand i: the columns', then the rows'
+                const uint8_t* at = lds + (s % S::kRing) * S::kStage;
+                if (i < NW) o.b[i] = S::B::read(at + S::A::kSize, wn * NW + i, step, lane);
+                else if (i < NW + LIVE) o.a[i - NW] = S::A::read(at, wm + WM * (i - NW), step, lane);
+            };
+            auto mfma = [&](const Operands& o, int i) __attribute__((always_inline)) {             // MFMA i of a step
+                if (i / NW < LIVE)
+                    acc[i / NW][i % NW] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(o.b[i % NW], o.a[i / NW], acc[i / NW][i % NW], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            __builtin_amdgcn_s_waitcnt(vmcnt_at_most((S::kRing - 1) * kAll));
             asm volatile("s_barrier" ::: "memory");
             __builtin_amdgcn_sched_barrier(0);
-            read(s + 1, 0, o0);
 #pragma unroll
-            for (int m = 0; m < MW; ++m) {
-                copy(s + S::kRing, m * kAll / MW, (m + 1) * kAll / MW);
-                mfma(o1, m);
+            for (int i = 0; i < kReads; ++i) read(0, i < kReads / 2 ? 0 : 1, i < kReads / 2 ? o0 : o1, i % (kReads / 2));
+            for (int s = 0; s < stages; ++s) {
+#pragma unroll
+                for (int i = 0; i < kSlots; ++i) {
+#pragma unroll
+                    for (int j = i * kReads / kSlots; j < (i + 1) * kReads / kSlots; ++j)
+                        read(s, j < kReads / 2 ? 2 : 3, j < kReads / 2 ? o2 : o3, j % (kReads / 2));
+                    mfma(o0, i);
+                }
+#pragma unroll
+                for (int i = 0; i < 2 * kSlots; ++i) {
+                    if (i == kFree) {
+                        __builtin_amdgcn_s_waitcnt(lgkmcnt_zero());
+                        asm volatile("s_barrier" ::: "memory");
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                    if (i >= kFree) copy(s + S::kRing, (i - kFree) * kAll / kCopySlots, (i - kFree + 1) * kAll / kCopySlots);
+                    mfma(i < kSlots ? o1 : o2, i % kSlots);
+                }
+                __builtin_amdgcn_s_waitcnt(vmcnt_at_most((S::kRing - 1) * kAll));
+                asm volatile("s_barrier" ::: "memory");
                 __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int i = 0; i < kSlots; ++i) {
+#pragma unroll
+                    for (int j = i * kReads / kSlots; j < (i + 1) * kReads / kSlots; ++j)
+                        read(s + 1, j < kReads / 2 ? 0 : 1, j < kReads / 2 ? o0 : o1, j % (kReads / 2));
+                    mfma(o3, i);
+                }
+            }
+            // the copies of the stages behind the last still write (zeros) to the LDS
+            __builtin_amdgcn_s_waitcnt(vmcnt_at_most(0) & lgkmcnt_zero());
+            __syncthreads();
+        }
+        uint8_t* slab = lds + wave * S::kSlab;
+        const int c0 = n0 + 32 * NW * wn;
+#pragma unroll
+        for (int m = 0; m < LIVE; ++m) {
+            const int r0 = 32 * (wm + WM * m);
+            if (r0 >= left || c0 >= a.N) continue;
+            uint8_t* out = a.out + (KIND == kGgWeight ? b.e * a.out_group + (m0 + r0) * a.out_stride
+                                                      : (b.row + (int64_t)m0 + r0) * a.out_stride);
+            gg_store<NW, F32, ADD>(out + (int64_t)c0 * (F32 ? 4 : 2), a.out_stride, a.out_vec, slab, acc[m], live - r0, left - r0,
+                                   a.N - c0, lane);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        // rows of padding behind those tiles
+        if constexpr (KIND != kGgWeight) {
+            for (int r = 32 * WM * LIVE + wm; r < left && r < S::kBM; r += WM) {
+                uint8_t* out = a.out + (b.row + (int64_t)m0 + r) * a.out_stride;
+                for (int n = c0 + lane; n < c0 + 32 * NW && n < a.N; n += 64) {
+                    if constexpr (F32) reinterpret_cast<float*>(out)[n] = 0.0f;
+                    else reinterpret_cast<uint16_t*>(out)[n] = 0;
+                }
             }
         }
-        // the copies of the stages behind the last still write (zeros) to the LDS
-        __builtin_amdgcn_s_waitcnt(vmcnt_at_most(0) & lgkmcnt_zero());
-        __syncthreads();
-    }
-
-    uint8_t* slab = lds + wave * 32 * kOutRow;
-    const int c0 = n0 + 32 * NW * wn;
-    const int es = F32 ? 4 : 2;
-#pragma unroll
-    for (int m = 0; m < MW; ++m) {
-        const int r0 = 32 * (wm * MW + m);
-        uint8_t* out = a.out + (KIND == kGgWeight ? g.e * a.out_group + (m0 + r0) * a.out_stride
-                                                  : (g.first + (int64_t)m0 + r0) * a.out_stride) + (int64_t)c0 * es;
-        if constexpr (ADD) gg_add<NW, F32>(out, a.out_stride, slab, acc[m], left - r0, a.N - c0, lane);
-        else gg_store<NW, F32, false>(out, a.out_stride, a.out_vec, slab, acc[m], live - r0, left - r0, a.N - c0, lane);
-    }
+    };
+    const int tiles = (live + 32 * WM - 1) / (32 * WM);
+    if (MW >= 4 && tiles >= 4) compute(std::integral_constant<int, (MW >= 4 ? 4 : 1)>());
+    else if (MW >= 3 && tiles >= 3) compute(std::integral_constant<int, (MW >= 3 ? 3 : 1)>());
+    else if (MW >= 2 && tiles >= 2) compute(std::integral_constant<int, (MW >= 2 ? 2 : 1)>());
+    else compute(std::integral_constant<int, 1>());
 }
 
 // ------------------------------------------------------------------ host side
+template <int KIND, int WM, int MW, int NW, bool F32, bool ADD>
+int launch_grouped(GgArgs a, hipStream_t s, const char* name) {
+    using S = GgShape<KIND, WM, MW, NW, F32, ADD>;
+    const int64_t nt = (a.N + S::kBN - 1) / S::kBN;
+    const int64_t row_blocks = a.R / S::kBM + (a.R < a.E ? a.R : a.E);      // whole blocks, and each expert's last
+    const int64_t blocks = KIND == kGgWeight ? (int64_t)a.E * ((a.M + S::kBM - 1) / S::kBM) * nt : row_blocks * nt;
+    const int64_t grid = (blocks + 7) / 8 * 8;
+    if (!launch_fits(grid, 256)) return fail(MOE_EUNSUPPORTED, "%s: too many output tiles", name);
+    a.row_blocks = (int)row_blocks;
+    hipLaunchKernelGGL((grouped_gemm_kernel<KIND, WM, MW, NW, F32, ADD>), dim3((unsigned)grid), dim3(256), 0, s, a);
+    return check_launch(name);
+}
+
 template <int KIND, int WM, int MW, int NW>
 int launch_grouped(const GgArgs& a, bool f32, bool add, hipStream_t s, const char* name) {
-    using S = GgShape<KIND, WM, MW, NW>;
-    const int64_t nt = (a.N + S::kBN - 1) / S::kBN;
-    int64_t tiles;
-    if (KIND == kGgWeight) tiles = (int64_t)a.E * ((a.M + S::kBM - 1) / S::kBM) * nt;
-    else tiles = (a.R / S::kBM + (a.R < a.E ? a.R : a.E)) * nt;     // whole blocks, and each expert's last
-    if (!launch_fits(tiles, 256)) return fail(MOE_EUNSUPPORTED, "%s: too many output tiles", name);
-    const dim3 g((unsigned)tiles), b(256);
     if constexpr (KIND == kGgWeight) {
-        if (add) {
-            if (f32) hipLaunchKernelGGL((grouped_gemm_kernel<KIND, WM, MW, NW, true, true>), g, b, 0, s, a);
-            else hipLaunchKernelGGL((grouped_gemm_kernel<KIND, WM, MW, NW, false, true>), g, b, 0, s, a);
-            return check_launch(name);
-        }
+        if (add) return f32 ? launch_grouped<KIND, WM, MW, NW, true, true>(a, s, name) : launch_grouped<KIND, WM, MW, NW, false, true>(a, s, name);
     }
-    if (f32) hipLaunchKernelGGL((grouped_gemm_kernel<KIND, WM, MW, NW, true, false>), g, b, 0, s, a);
-    else hipLaunchKernelGGL((grouped_gemm_kernel<KIND, WM, MW, NW, false, false>), g, b, 0, s, a);
-    return check_launch(name);
+    return f32 ? launch_grouped<KIND, WM, MW, NW, true, false>(a, s, name) : launch_grouped<KIND, WM, MW, NW, false, false>(a, s, name);
 }
 
 // Sizes of the three calls.
@@ -412,6 +474,33 @@ static int gg_sizes(int64_t rows_max, int E, int N, int D, int dtype, const char
     if (N % 8 || D % 8 || N > MOE_MAX_GROUPED || D > MOE_MAX_GROUPED)
         return fail(MOE_EUNSUPPORTED, "%s: N=%d and D=%d must be multiples of 8 up to %d", name, N, D, MOE_MAX_GROUPED);
     return MOE_OK;
+}
+
+// Whether the last round of blocks, one a CU, is 0.8 full or one of many.
+static bool gg_filled(int64_t blocks) { return blocks >= 1024 || 10 * blocks >= 8 * ((blocks + 255) / 256 * 256); }
+
+// The block's rows for the forward product and the input's gradient. Wide blocks
+// read less per product, from the L2 and of the weights; but a CU without one
+// idles, and where an expert has few rows a block is mostly empty (its empty row
+// tiles are not computed). rows_max counts padding and routes that went elsewhere:
+// the experts' rows are only guessed from it. us, blocks of 256 x 256, 128 x 128
+// and 32 x 128, forward and input gradient:
+//   E x N x D        rows each
+//   128 x 4096 x 1536  256   620 579   609 569   1253 1144     8 x 4096 x 1536   4096   370 348   431 415   862 881
+//   128 x 4096 x 1536   32   301 281   305 300    334  325    64 x 1536 x 2048   128   104  84   112 109   161 169
+//    64 x 1536 x 2048   64   100  76    87  85    109  110    64 x 1536 x 2048    16    93  73    81  77    80  77
+//     8 x 1536 x 2048  256    41  37    20  24     34   40     8 x 1536 x 2048    64    32  27    19  16    13  17
+//     1 x 4096 x 4096 1024    75  81    37  38     71   79     1 x 4096 x 4096   256    72  80    32  33    22  28
+//   128 x 4096 x 1536    4 in the mean, skewed      -     -     121 133   117 129
+static int gg_rows_blocks(int64_t rows_max, int E, int cols) {
+    const auto blocks = [&](int64_t side) {         // about: half a block of rows is lost an expert
+        const int64_t rows = rows_max / side + (rows_max < E ? rows_max : E) / 2, least = rows_max < E ? rows_max : E;
+        return (rows > least ? rows : least) * ((cols + side - 1) / side);
+    };
+    const int64_t wide = blocks(256);
+    if (rows_max >= 32 * (int64_t)E && wide >= 200 && (wide >= 448 || (rows_max >= 96 * (int64_t)E && gg_filled(wide)))) return 256;
+    if (rows_max >= 32 * (int64_t)E && blocks(128) >= 150) return 128;
+    return 32;
 }
 
 // Row strides of the operands: at least the row, whole 16-byte pieces, and a block's rows within 31 bits.
@@ -443,9 +532,11 @@ static int gg_rows_call(const uint16_t* x, int64_t x_row_stride, const uint16_t*
     const bool f32 = out_dtype == MOE_F32;
     a.out = (uint8_t*)out; a.out_stride = out_row_stride * (f32 ? 4 : 2); a.out_vec = a.out_stride % 16 == 0;
     hipStream_t s = (hipStream_t)stream;
-    if (rows_max >= 128 * (int64_t)E)
-        return input_grad ? launch_grouped<kGgRowsT, 2, 4, 4>(a, f32, false, s, name) : launch_grouped<kGgRows, 2, 4, 4>(a, f32, false, s, name);
-    return input_grad ? launch_grouped<kGgRowsT, 1, 1, 1>(a, f32, false, s, name) : launch_grouped<kGgRows, 1, 1, 1>(a, f32, false, s, name);
+    switch (gg_rows_blocks(rows_max, E, out_cols)) {
+        case 256: return input_grad ? launch_grouped<kGgRowsT, 2, 4, 4>(a, f32, false, s, name) : launch_grouped<kGgRows, 2, 4, 4>(a, f32, false, s, name);
+        case 128: return input_grad ? launch_grouped<kGgRowsT, 2, 2, 2>(a, f32, false, s, name) : launch_grouped<kGgRows, 2, 2, 2>(a, f32, false, s, name);
+        default: return input_grad ? launch_grouped<kGgRowsT, 1, 1, 1>(a, f32, false, s, name) : launch_grouped<kGgRows, 1, 1, 1>(a, f32, false, s, name);
+    }
 }
 
 }  // namespace moe
@@ -483,7 +574,11 @@ extern "C" int moe_grouped_gemm_wgrad(const uint16_t* d_out, int64_t d_out_row_s
     a.b = (const uint8_t*)x; a.b_stride = 2 * x_row_stride;
     a.offsets = expert_offsets; a.counts = expert_counts; a.E = E; a.R = rows_max; a.M = N; a.N = D;
     a.out = (uint8_t*)d_w; a.out_stride = (int64_t)D * (f32 ? 4 : 2); a.out_group = a.out_stride * N; a.out_vec = a.out_stride % 16 == 0;
-    if ((int64_t)E * ((N + 127) / 128) * ((D + 127) / 128) >= 256)
+    // us, blocks of 256 x 256 and 128 x 128, bf16 d_w: 128 experts x 4096 x 1536, 256 rows each 664 and 774 (fp32 871
+    // and 1064), 32 rows 392 and 388, 4 rows in the mean 440 and 305; 64 x 1536 x 2048, 128 rows 133 and 124; 8 x 1536
+    // x 2048, 256 rows, 384 wide blocks on 256 CUs, 29.5 and 24.8; 8 x 4096 x 1536, 4096 rows, 350 and 438
+    const int64_t wide = (int64_t)E * ((N + 255) / 256) * ((D + 255) / 256);
+    if (rows_max >= 192 * (int64_t)E && wide >= 200 && gg_filled(wide))
         return launch_grouped<kGgWeight, 2, 4, 4>(a, f32, accumulate != 0, (hipStream_t)stream, name);
-    return launch_grouped<kGgWeight, 2, 1, 1>(a, f32, accumulate != 0, (hipStream_t)stream, name);
+    return launch_grouped<kGgWeight, 2, 2, 2>(a, f32, accumulate != 0, (hipStream_t)stream, name);
 }
