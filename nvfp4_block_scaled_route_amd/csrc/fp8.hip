@@ -167,8 +167,11 @@ __global__ void __launch_bounds__(256) fp8_quant_weight_kernel(FwArgs a) {
 }
 
 // ------------------------------------------------------------------ product
+// A block of K is one 16 x 16 x 128 MFMA, from zero; its sum is added to the
+// accumulators under its scale, a's times w's, in fp32. With the weights as the
+// MFMA's rows a lane holds 4 columns of one token (lane & 15), all under one scale.
+// A lane's operand is 16 bytes at element 16 g and 16 at 64 + 16 g, g = lane / 16.
 typedef int fp_i8 __attribute__((ext_vector_type(8)));
-typedef float fp_f16v __attribute__((ext_vector_type(16)));
 
 struct FgArgs {
     const uint8_t* a;
@@ -183,171 +186,438 @@ struct FgArgs {
     int out_vec;
 };
 
+struct FpFrag {
+    uint4 q[2];
+    __device__ __forceinline__ fp_i8 reg() const {
+        return fp_i8{(int)q[0].x, (int)q[0].y, (int)q[0].z, (int)q[0].w, (int)q[1].x, (int)q[1].y, (int)q[1].z, (int)q[1].w};
+    }
+};
+
+__device__ __forceinline__ floatx4 fp_mfma(const FpFrag& w, const FpFrag& a) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w.reg(), a.reg(), floatx4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+}
+
+// ------------------------------------------------------------------ few tokens
+// A stream of the weights: a workgroup owns 16 columns, its 8 waves split the blocks
+// of K, and the waves' sums are added through LDS in wave order.
+constexpr int kFsWaves = 8;
+
+template <int TM>
+__global__ void __launch_bounds__(64 * kFsWaves) fp8_gemm_skinny_kernel(FgArgs a) {
+    constexpr int U = 4;            // blocks whose loads issue together
+    __shared__ floatx4 s_sum[kFsWaves][TM][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+    const int n0 = blockIdx.x * 16, blocks = (a.K + 127) / 128;
+    const uint8_t* wrow = a.w + (n0 + r < a.N ? n0 + r : a.N - 1) * a.w_row_stride + 16 * g;
+    const uint8_t* arow[TM];
+    const float* asf[TM];
+#pragma unroll
+    for (int m = 0; m < TM; ++m) {
+        const int t = 16 * m + r < a.T ? 16 * m + r : a.T - 1;
+        arow[m] = a.a + (int64_t)t * a.K + 16 * g;
+        asf[m] = a.a_sf + t;
+    }
+    const float* wsf = a.w_sf + (int64_t)(n0 / 128) * blocks;       // 16 columns lie in one block
+    floatx4 acc[TM];
+#pragma unroll
+    for (int m = 0; m < TM; ++m) acc[m] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+    const int per = (blocks + kFsWaves - 1) / kFsWaves, b0 = wave * per, b1 = b0 + per < blocks ? b0 + per : blocks;
+    for (int b = b0; b < b1; b += U) {
+        FpFrag fw[U], fa[U][TM];
+        float sa[U][TM], sw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int left = b + u < b1 ? a.K - 128 * (b + u) - 16 * g : 0;     // bytes of K from this lane's on
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t at = 128 * (int64_t)(b + u) + 64 * h;
+                fw[u].q[h] = left > 64 * h ? *reinterpret_cast<const uint4*>(wrow + at) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                for (int m = 0; m < TM; ++m)
+                    fa[u][m].q[h] = left > 64 * h ? *reinterpret_cast<const uint4*>(arow[m] + at) : make_uint4(0u, 0u, 0u, 0u);
+            }
+            sw[u] = b + u < b1 ? wsf[b + u] : 0.0f;
+#pragma unroll
+            for (int m = 0; m < TM; ++m) sa[u][m] = b + u < b1 ? asf[m][(b + u) * a.a_sf_stride] : 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int m = 0; m < TM; ++m) {
+                const float f = __fmul_rn(sa[u][m], sw[u]);
+                const floatx4 t = fp_mfma(fw[u], fa[u][m]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[m][i] = __fmaf_rn(f, t[i], acc[m][i]);
+            }
+    }
+#pragma unroll
+    for (int m = 0; m < TM; ++m) s_sum[wave][m][lane] = acc[m];
+    __syncthreads();
+    if (wave >= TM) return;
+    floatx4 sum = s_sum[0][wave][lane];
+#pragma unroll
+    for (int w = 1; w < kFsWaves; ++w) sum += s_sum[w][wave][lane];
+    const int t = 16 * wave + r, n = n0 + 4 * g;
+    if (t >= a.T) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (n + i < a.N) a.out[t * a.out_stride + n + i] = (uint16_t)f32_to_bf16(sum[i]);
+}
+
+// ------------------------------------------------------------------ many tokens
 // Direct-to-LDS load of one word a lane, as lds_copy16.
 __device__ __forceinline__ void fp_copy4(u32x4 rsrc, uint32_t lds, uint32_t voff, uint32_t soff) {
     asm volatile("buffer_load_dword %0, %1, %2 offen lds" :: "v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds) : "memory");
 }
 
-template <int WM, int WN, int MW, int NW>
-struct FgShape {
-    static constexpr int kWaves = WM * WN, kBM = 32 * WM * MW, kBN = 32 * WN * NW;
-    static constexpr int kACopies = kBM * 128 / (1024 * kWaves), kWCopies = kBN * 128 / (1024 * kWaves), kAll = kACopies + kWCopies + 1;
-    static constexpr int kSfBytes = kBM < 64 ? 256 : 4 * kBM;
-    static constexpr int kW = kBM * 128, kSf = kW + kBN * 128, kStage = kSf + kSfBytes;
-    static constexpr int kPerCu = kBM * kBN >= 256 * 256 ? 1 : 2;
-    static constexpr int kFit = 160 * 1024 / kPerCu / kStage, kRing = kFit < 6 ? kFit : 6;
-    static_assert(kRing >= 2 && (kRing - 1) * kAll < 64 && kACopies >= 1 && kWCopies >= 1, "ring of stages");
-};
+// *p, or 0, waited for here: a wait at the use, which the compiler would put into
+// every stage, would wait for the copies issued since too.
+__device__ __forceinline__ float fp_load_wait(const float* p, bool on) {
+    float v = on ? *p : 0.0f;
+    asm volatile("" : "+v"(v));
+    return v;
+}
 
-__device__ __forceinline__ int fp_swizzle(int chunk, int row) { return chunk ^ (row & 7) ^ ((row >> 3) & 1); }
+// LDS rows of NB blocks (128 or 256 bytes): the 16-byte chunks of a row permuted so
+// that 16 consecutive rows' reads of one chunk spread over all banks.
+template <int NB>
+__device__ __forceinline__ int fp_swizzle(int chunk, int row) {
+    return NB == 2 ? chunk ^ (row & 15) : chunk ^ (row & 7) ^ ((row >> 3) & 1);
+}
 
-// A stage is one block of K: 128 bytes of every row. The block's products are summed
-// by the matrix cores from zero, and the sum is added to the accumulators under its
-// scale, a's times w's: with the weights as the MFMA's rows a lane holds 16 columns
-// of one token, all under one scale.
-template <int WM, int WN, int MW, int NW>
-__global__ void __launch_bounds__(64 * WM * WN, (FgShape<WM, WN, MW, NW>::kPerCu * WM * WN / 4)) fp8_gemm_kernel(FgArgs a) {
-    using S = FgShape<WM, WN, MW, NW>;
-    constexpr int kOutRow = 64 * NW + 16, kLds = S::kRing * S::kStage > S::kWaves * 32 * kOutRow ? S::kRing * S::kStage : S::kWaves * 32 * kOutRow;
-    __shared__ __align__(16) uint8_t lds[kLds];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int r = lane & 31, g = lane >> 5, wm = wave / WN, wn = wave % WN;
-    const int mt = (a.T + S::kBM - 1) / S::kBM, nt = (a.N + S::kBN - 1) / S::kBN, tiles = mt * nt;
+// One workgroup's block of the output. Blocks of the output to workgroups: each XCD
+// (workgroups are dealt to the 8 round robin) gets a contiguous run of them, which
+// goes through groups of 4 rows of blocks column by column.
+__device__ __forceinline__ void fp_block_of(int T, int N, int bm, int bn, int& m0, int& n0) {
+    const int mt = (T + bm - 1) / bm, nt = (N + bn - 1) / bn, tiles = mt * nt;
     const int x = blockIdx.x & 7, per = tiles >> 3, more = tiles & 7;
     const int id = x * per + (x < more ? x : more) + (int)(blockIdx.x >> 3);
     const int gm0 = id / (4 * nt) * 4, gh = mt - gm0 < 4 ? mt - gm0 : 4, in = id - gm0 * nt;
-    const int m0 = (gm0 + in % gh) * S::kBM, n0 = (in / gh) * S::kBN;
+    m0 = (gm0 + in % gh) * bm, n0 = (in / gh) * bn;
+}
 
-    const int stages = (a.K + 127) / 128;
-    const u32x4 ra = buffer_desc(a.a + (int64_t)m0 * a.K), rw = buffer_desc(a.w + n0 * a.w_row_stride), rs = buffer_desc(a.a_sf + m0);
-    uint32_t offa[S::kACopies], offw[S::kWCopies], offs;
-    const int r0 = 8 * wave + lane / 8, chunk = fp_swizzle(lane % 8, r0);
+// 16 tokens of a wave's 16 NW columns, turned in the wave's own part of the LDS to
+// whole pieces of their rows.
+template <int NW>
+__device__ __forceinline__ void fp_store(const FgArgs& a, uint8_t* slab, const floatx4 (&acc)[NW], int t0, int c0, int lane) {
+    constexpr int kOutRow = 32 * NW + 16;
+    const int r = lane & 15, g = lane >> 4;
+    wave_lds_sync();
 #pragma unroll
-    for (int q = 0; q < S::kACopies; ++q) {
-        const int row = r0 + 8 * S::kWaves * q;
-        offa[q] = m0 + row < a.T ? (uint32_t)(row * a.K + chunk * 16) : 0x80000000u;
-    }
+    for (int n = 0; n < NW; ++n)
+        *reinterpret_cast<uint2*>(slab + r * kOutRow + 2 * (16 * n + 4 * g)) =
+            make_uint2(bf16x2_pack(acc[n][0], acc[n][1]), bf16x2_pack(acc[n][2], acc[n][3]));
+    wave_lds_sync();
 #pragma unroll
-    for (int q = 0; q < S::kWCopies; ++q) {
-        const int row = r0 + 8 * S::kWaves * q;
-        offw[q] = n0 + row < a.N ? (uint32_t)(row * a.w_row_stride + chunk * 16) : 0x80000000u;
-    }
-    const int part = wave % (S::kSfBytes / 256), srow = part * 64 + lane;
-    offs = srow < S::kBM && m0 + srow < a.T ? (uint32_t)(4 * srow) : 0x80000000u;
-    const uint32_t lds0 = lds_addr(lds);
-    auto copy = [&](int s, int q0, int q1) {
-        const uint32_t at = lds0 + (s % S::kRing) * S::kStage;
-        const bool in_k = s * 128 + chunk * 16 < a.K;
-#pragma unroll
-        for (int q = q0; q < q1; ++q) {
-            if (q < S::kACopies)
-                lds_copy16(ra, __builtin_amdgcn_readfirstlane(at + (S::kWaves * q + wave) * 1024), in_k ? offa[q] : 0x80000000u, s * 128);
-            else if (q < S::kACopies + S::kWCopies)
-                lds_copy16(rw, __builtin_amdgcn_readfirstlane(at + S::kW + (S::kWaves * (q - S::kACopies) + wave) * 1024),
-                           in_k ? offw[q - S::kACopies] : 0x80000000u, s * 128);
-            else        // the stage's scales; waves repeat each other's
-                fp_copy4(buffer_desc(a.a_sf + m0 + (s < stages ? s : 0) * a.a_sf_stride),
-                         __builtin_amdgcn_readfirstlane(at + S::kSf + part * 256), offs, 0u);
-        }
-    };
-    struct Frag {
-        uint4 q[2];
-        __device__ __forceinline__ fp_i8 reg() const {
-            return fp_i8{(int)q[0].x, (int)q[0].y, (int)q[0].z, (int)q[0].w, (int)q[1].x, (int)q[1].y, (int)q[1].z, (int)q[1].w};
-        }
-    };
-    auto read = [&](const uint8_t* rows, int row, Frag (&f)[2]) {
-        const uint8_t* p = rows + row * 128;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) f[h].q[i] = *reinterpret_cast<const uint4*>(p + 16 * fp_swizzle(4 * h + 2 * i + g, row));
-    };
-    // this wave's columns lie in one block of w's scales; lane i holds that of stage 64 j + i
-    const float* wsf = a.w_sf + (int64_t)((n0 + 32 * NW * wn) / 128) * stages;
-    const bool cols = n0 + 32 * NW * wn < a.N;
-    float sw64 = 0.0f;
-
-    fp_f16v acc[MW][NW];
-#pragma unroll
-    for (int m = 0; m < MW; ++m)
-#pragma unroll
-        for (int n = 0; n < NW; ++n)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[m][n][i] = 0.0f;
-
-#pragma unroll
-    for (int s = 0; s < S::kRing; ++s) copy(s, 0, S::kAll);
-    Frag fw[NW][2], fa[MW][2];
-    float sa[MW];
-    __builtin_amdgcn_s_waitcnt(vmcnt_at_most((S::kRing - 1) * S::kAll));
-    __syncthreads();
-    for (int s = 0; s < stages; ++s) {
-        const uint8_t* at = lds + (s % S::kRing) * S::kStage;
-        if ((s & 63) == 0) sw64 = cols && s + lane < stages ? wsf[s + lane] : 0.0f;
-#pragma unroll
-        for (int n = 0; n < NW; ++n) read(at + S::kW, 32 * (wn * NW + n) + r, fw[n]);
-#pragma unroll
-        for (int m = 0; m < MW; ++m) {
-            read(at, 32 * (wm * MW + m) + r, fa[m]);
-            sa[m] = *reinterpret_cast<const float*>(at + S::kSf + 4 * (32 * (wm * MW + m) + r));
-        }
-        const float sw = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(sw64), s & 63));
-#pragma unroll
-        for (int m = 0; m < MW; ++m) {
-            if (m == MW - 1) {
-                __builtin_amdgcn_s_waitcnt(vmcnt_at_most((S::kRing - 2) * S::kAll) & lgkmcnt_zero());
-                asm volatile("s_barrier" ::: "memory");
-                copy(s + S::kRing, 0, S::kAll);
-            }
-            const float f = __fmul_rn(sa[m], sw);
-#pragma unroll
-            for (int n = 0; n < NW; ++n) {
-                fp_f16v t = {};
-                t = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[n][0].reg(), fa[m][0].reg(), t, 0, 0, 0, 0, 0, 0);
-                t = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fw[n][1].reg(), fa[m][1].reg(), t, 0, 0, 0, 0, 0, 0);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) acc[m][n][i] = __fmaf_rn(f, t[i], acc[m][n][i]);
-            }
-        }
-    }
-    __builtin_amdgcn_s_waitcnt(vmcnt_at_most(0) & lgkmcnt_zero());
-    __syncthreads();
-
-    uint8_t* slab = lds + wave * 32 * kOutRow;
-#pragma unroll
-    for (int m = 0; m < MW; ++m) {
-        wave_lds_sync();
-#pragma unroll
-        for (int n = 0; n < NW; ++n)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                *reinterpret_cast<uint2*>(slab + r * kOutRow + 2 * (32 * n + 8 * q + 4 * g)) =
-                    make_uint2(f32_to_bf16(acc[m][n][4 * q]) | (f32_to_bf16(acc[m][n][4 * q + 1]) << 16),
-                               f32_to_bf16(acc[m][n][4 * q + 2]) | (f32_to_bf16(acc[m][n][4 * q + 3]) << 16));
-        wave_lds_sync();
-        const int t0 = m0 + 32 * (wm * MW + m), c0 = n0 + 32 * NW * wn;
-#pragma unroll
-        for (int j = 0; j < 2 * NW; ++j) {
-            const int i = lane + 64 * j, row = i / (4 * NW), c = i % (4 * NW) * 8;
-            if (t0 + row >= a.T || c0 + c >= a.N) continue;
-            uint16_t* dst = a.out + (t0 + row) * a.out_stride + c0 + c;
-            const uint16_t* src = reinterpret_cast<const uint16_t*>(slab + row * kOutRow + 2 * c);
-            if (a.out_vec && c0 + c + 8 <= a.N) {
-                *reinterpret_cast<u32x4*>(dst) = *reinterpret_cast<const u32x4*>(src);
-            } else {
-                for (int k = 0; k < 8 && c0 + c + k < a.N; ++k) dst[k] = src[k];
-            }
+    for (int j = 0; j < (NW + 1) / 2; ++j) {        // 2 NW pieces of 16 bytes a row
+        const int i = lane + 64 * j, row = i / (2 * NW), c = i % (2 * NW) * 8;
+        if (row >= 16 || t0 + row >= a.T || c0 + c >= a.N) continue;
+        uint16_t* dst = a.out + (t0 + row) * a.out_stride + c0 + c;
+        const uint16_t* src = reinterpret_cast<const uint16_t*>(slab + row * kOutRow + 2 * c);
+        if (a.out_vec && c0 + c + 8 <= a.N) {
+            __builtin_nontemporal_store(*reinterpret_cast<const u32x4*>(src), reinterpret_cast<u32x4*>(dst));
+        } else {
+            for (int k = 0; k < 8 && c0 + c + k < a.N; ++k) dst[k] = src[k];
         }
     }
 }
 
-template <int WM, int WN, int MW, int NW>
+// 4 waves, 2 x 2, each MW x NW tiles of 16 x 16; a stage is NB blocks of K.
+template <int MW, int NW, int NB>
+struct FgShape {
+    static constexpr int kBM = 32 * MW, kBN = 32 * NW, kRow = 128 * NB;
+    static constexpr int kACopies = kBM * kRow / 4096, kWCopies = kBN * kRow / 4096, kAll = kACopies + kWCopies + 1;
+    static constexpr int kParts = kBM / 64;             // of 64 tokens' scales
+    static constexpr int kW = kBM * kRow, kSf = kW + kBN * kRow, kStage = kSf + NB * 4 * kBM;
+    static constexpr int kFit = 80 * 1024 / kStage, kRing = kFit < 4 ? kFit : 4;
+    static constexpr int kSlab = 16 * (32 * NW + 16), kLds = kRing * kStage > 4 * kSlab ? kRing * kStage : 4 * kSlab;
+    static_assert(kRing >= 2 && kRing * kAll < 64 && kBM % 64 == 0 && kParts * NB <= 4 && 128 % (16 * NW) == 0, "ring of stages");
+};
+
+// The operands of a stage are read from LDS into registers while the products of
+// the stage before run, so its buffer is free a stage early, and one barrier a
+// stage does.
+template <int MW, int NW, int NB>
+__global__ void __launch_bounds__(256, 2) fp8_gemm_kernel(FgArgs a) {
+    using S = FgShape<MW, NW, NB>;
+    __shared__ __align__(16) uint8_t lds[S::kLds];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, g = lane >> 4, wm = wave >> 1, wn = wave & 1;
+    int m0, n0;
+    fp_block_of(a.T, a.N, S::kBM, S::kBN, m0, n0);
+
+    const int blocks = (a.K + 127) / 128, stages = (blocks + NB - 1) / NB;
+    const u32x4 ra = buffer_desc(a.a + (int64_t)m0 * a.K), rw = buffer_desc(a.w + n0 * a.w_row_stride);
+    constexpr int kRowsPer = 8 / NB;        // rows that an instruction copies
+    const int r0 = kRowsPer * wave + lane / (8 * NB), chunk = fp_swizzle<NB>(lane % (8 * NB), r0);      // rows 4 kRowsPer apart have the same
+    const uint32_t offa = (uint32_t)(r0 * a.K + chunk * 16), offw = (uint32_t)(r0 * a.w_row_stride + chunk * 16);
+    const int rows_a = a.T - m0 - r0, rows_w = a.N - n0 - r0;
+    const int piece = wave % (S::kParts * NB), sblock = piece / S::kParts, stok = piece % S::kParts * 64 + lane;
+    const uint32_t offs = m0 + stok < a.T ? (uint32_t)(4 * stok) : 0x80000000u;
+    const uint32_t lds0 = lds_addr(lds);
+    auto copy = [&](int s) __attribute__((always_inline)) {
+        const uint32_t at = lds0 + (s % S::kRing) * S::kStage;
+        const bool in_k = s * S::kRow + chunk * 16 < a.K;
+#pragma unroll
+        for (int q = 0; q < S::kACopies; ++q)
+            lds_copy16(ra, __builtin_amdgcn_readfirstlane(at + (4 * q + wave) * 1024),
+                       in_k && 4 * kRowsPer * q < rows_a ? offa + (uint32_t)(4 * kRowsPer * q * a.K) : 0x80000000u, s * S::kRow);
+#pragma unroll
+        for (int q = 0; q < S::kWCopies; ++q)
+            lds_copy16(rw, __builtin_amdgcn_readfirstlane(at + S::kW + (4 * q + wave) * 1024),
+                       in_k && 4 * kRowsPer * q < rows_w ? offw + (uint32_t)(4 * kRowsPer * q * a.w_row_stride) : 0x80000000u, s * S::kRow);
+        const int b = s * NB + sblock;      // the tokens' scales; waves may repeat each other's
+        fp_copy4(buffer_desc(a.a_sf + m0 + (b < blocks ? b : 0) * a.a_sf_stride), __builtin_amdgcn_readfirstlane(at + S::kSf + piece * 256),
+                 b < blocks ? offs : 0x80000000u, 0u);
+    };
+    struct Operands {
+        FpFrag w[NB][NW], a[NB][MW];
+        float sa[NB][MW];
+    };
+    auto read = [&](int s, Operands& o) __attribute__((always_inline)) {
+        const uint8_t* at = lds + (s % S::kRing) * S::kStage;
+        auto frag = [&](const uint8_t* rows, int row, int b) __attribute__((always_inline)) {
+            FpFrag f;
+            f.q[0] = *reinterpret_cast<const uint4*>(rows + row * S::kRow + 16 * fp_swizzle<NB>(8 * b + g, row));
+            f.q[1] = *reinterpret_cast<const uint4*>(rows + row * S::kRow + 16 * fp_swizzle<NB>(8 * b + 4 + g, row));
+            return f;
+        };
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+#pragma unroll
+            for (int n = 0; n < NW; ++n) o.w[b][n] = frag(at + S::kW, 16 * (wn * NW + n) + r, b);
+#pragma unroll
+            for (int m = 0; m < MW; ++m) {
+                const int row = 16 * (wm * MW + m) + r;
+                o.a[b][m] = frag(at, row, b);
+                o.sa[b][m] = *reinterpret_cast<const float*>(at + S::kSf + 4 * (b * S::kBM + row));
+            }
+        }
+    };
+    // this wave's columns lie in one block of w's scales; lane i holds that of block 64 j + i
+    const float* wsf = a.w_sf + (int64_t)((n0 + 16 * NW * wn) / 128) * blocks;
+    const bool cols = n0 + 16 * NW * wn < a.N;
+    float sw64 = 0.0f;
+    floatx4 acc[MW][NW];
+#pragma unroll
+    for (int m = 0; m < MW; ++m)
+#pragma unroll
+        for (int n = 0; n < NW; ++n) acc[m][n] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+    auto stage = [&](int s, const Operands& o, Operands& next) __attribute__((always_inline)) {
+        __builtin_amdgcn_s_waitcnt(vmcnt_at_most((S::kRing - 2) * S::kAll) & lgkmcnt_zero());
+        asm volatile("s_barrier" ::: "memory");
+        copy(s + S::kRing);
+        read(s + 1, next);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const float sw = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(sw64), (s * NB + b) & 63));
+#pragma unroll
+            for (int m = 0; m < MW; ++m) {
+                floatx4 t[NW];
+#pragma unroll
+                for (int n = 0; n < NW; ++n) t[n] = fp_mfma(o.w[b][n], o.a[b][m]);
+                const float f = __fmul_rn(o.sa[b][m], sw);
+#pragma unroll
+                for (int n = 0; n < NW; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[m][n][i] = __fmaf_rn(f, t[n][i], acc[m][n][i]);
+            }
+        }
+    };
+    static_assert(64 % (2 * NB) == 0, "a pair of stages lies in 64 blocks");
+#pragma unroll
+    for (int s = 0; s < S::kRing; ++s) copy(s);
+    Operands o0, o1;
+    __builtin_amdgcn_s_waitcnt(vmcnt_at_most((S::kRing - 1) * S::kAll));
+    __syncthreads();
+    read(0, o0);
+    for (int s = 0; s < stages; s += 2) {
+        if ((s * NB & 63) == 0) sw64 = fp_load_wait(wsf + s * NB + lane, cols && s * NB + lane < blocks);
+        stage(s, o0, o1);
+        if (s + 1 < stages) stage(s + 1, o1, o0);
+    }
+    // the copies of the stages behind the last still write to the LDS
+    __builtin_amdgcn_s_waitcnt(vmcnt_at_most(0) & lgkmcnt_zero());
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < MW; ++m) {
+        const int t0 = m0 + 16 * (wm * MW + m);
+        if (t0 < a.T && cols) fp_store<NW>(a, lds + wave * S::kSlab, acc[m], t0, n0 + 16 * NW * wn, lane);
+    }
+}
+
+// 256 x 256: 8 waves, 2 x 4, of 128 x 64, which leaves a wave no registers to read
+// a stage's operands beside the products of the one before; so the waves take
+// turns: while 4 read, the other 4, one on each SIMD with them, multiply. Half steps
+// end in barriers. Waves 0 to 3 read stage s in half step 2 s (the weights and their
+// first 4 tiles of tokens; the other 4 while they multiply) and multiply in 2 s + 1,
+// waves 4 to 7 one half step later. So stage s + 2 may be copied into s's buffer
+// from half step 2 s + 2 on, but for the rows of the other tiles, which are read
+// until its end, and come in 2 s + 3: the waves that read issue the copies, waves 0
+// to 3 the first part and the others the second, and either has two half steps to
+// arrive. The tokens' scales have 4 buffers.
+//
+// A SIMD's MFMA takes 32 cycles and the 4 additions of its sum 16, which do not run
+// beside it: 2/3 of the matrix unit's rate is the most.
+struct FgWide {
+    static constexpr int kSide = 256, kW = 256 * 128, kStage = 2 * 256 * 128, kSf = 2 * kStage, kLds = kSf + 4 * 1024;
+};
+
+__global__ void __launch_bounds__(512, 2) fp8_gemm_wide_kernel(FgArgs a) {
+    using S = FgWide;
+    __shared__ __align__(16) uint8_t lds[S::kLds];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, g = lane >> 4, wm = wave >> 2, wn = wave & 3;
+    int m0, n0;
+    fp_block_of(a.T, a.N, S::kSide, S::kSide, m0, n0);
+
+    const int stages = (a.K + 127) / 128;
+    const u32x4 ra = buffer_desc(a.a + (int64_t)m0 * a.K), rw = buffer_desc(a.w + n0 * a.w_row_stride);
+    const int r0 = 8 * wn + lane / 8, chunk = fp_swizzle<1>(lane % 8, r0);          // rows 32 apart have the same
+    const uint32_t lds0 = lds_addr(lds);
+    const uint32_t offa = (uint32_t)(r0 * a.K + chunk * 16), offw = (uint32_t)(r0 * a.w_row_stride + chunk * 16);
+    const int rows_a = a.T - m0 - r0, rows_w = a.N - n0 - r0;
+    // Rows [32 q, 32 q + 32) of a stage, by the 4 waves of a group.
+    auto copy_a = [&](int s, int q) __attribute__((always_inline)) {
+        lds_copy16(ra, __builtin_amdgcn_readfirstlane(lds0 + (s & 1) * S::kStage + (4 * q + wn) * 1024),
+                   s * 128 + chunk * 16 < a.K && 32 * q < rows_a ? offa + (uint32_t)(32 * q * a.K) : 0x80000000u, s * 128);
+    };
+    auto copy_first = [&](int s) __attribute__((always_inline)) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            lds_copy16(rw, __builtin_amdgcn_readfirstlane(lds0 + (s & 1) * S::kStage + S::kW + (4 * q + wn) * 1024),
+                       s * 128 + chunk * 16 < a.K && 32 * q < rows_w ? offw + (uint32_t)(32 * q * a.w_row_stride) : 0x80000000u, s * 128);
+        copy_a(s, 0);
+        copy_a(s, 1);
+        copy_a(s, 4);
+        copy_a(s, 5);
+        const int tok = wn * 64 + lane;
+        fp_copy4(buffer_desc(a.a_sf + m0 + (s < stages ? s : 0) * a.a_sf_stride),
+                 __builtin_amdgcn_readfirstlane(lds0 + S::kSf + (s & 3) * 1024 + wn * 256),
+                 s < stages && m0 + tok < a.T ? (uint32_t)(4 * tok) : 0x80000000u, 0u);
+    };
+    auto copy_second = [&](int s) __attribute__((always_inline)) {
+        copy_a(s, 2);
+        copy_a(s, 3);
+        copy_a(s, 6);
+        copy_a(s, 7);
+    };
+    FpFrag fw[4], fa[5];        // tile m of the tokens in fa[m % 5]
+    auto frag = [&](const uint8_t* rows, int row) __attribute__((always_inline)) {
+        FpFrag f;
+        f.q[0] = *reinterpret_cast<const uint4*>(rows + row * 128 + 16 * fp_swizzle<1>(g, row));
+        f.q[1] = *reinterpret_cast<const uint4*>(rows + row * 128 + 16 * fp_swizzle<1>(4 + g, row));
+        return f;
+    };
+    auto read = [&](int s) __attribute__((always_inline)) {
+        const uint8_t* at = lds + (s & 1) * S::kStage;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) fw[n] = frag(at + S::kW, 64 * wn + 16 * n + r);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) fa[m] = frag(at, 128 * wm + 16 * m + r);
+    };
+    const float* wsf = a.w_sf + (int64_t)((n0 + 64 * wn) / 128) * stages;
+    const bool cols = n0 + 64 * wn < a.N;
+    float sw64 = 0.0f;
+    floatx4 acc[8][4];
+#pragma unroll
+    for (int m = 0; m < 8; ++m)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) acc[m][n] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+    auto products = [&](int s) __attribute__((always_inline)) {
+        const uint8_t* at = lds + (s & 1) * S::kStage;
+        __builtin_amdgcn_s_setprio(1);
+        const float sw = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(sw64), s & 63));
+        const uint8_t* sf = lds + S::kSf + (s & 3) * 1024 + 4 * (128 * wm + r);
+        float f = 0.0f, last = 0.0f, sa = *reinterpret_cast<const float*>(sf);
+        floatx4 t[4];
+        // a sum is added two MFMAs after its own
+#pragma unroll
+        for (int i = 0; i < 34; ++i) {
+            const int m = i / 4, n = i % 4;
+            if (n == 0 && m < 8) {
+                last = f;
+                f = __fmul_rn(sa, sw);
+                if (m < 7) sa = *reinterpret_cast<const float*>(sf + 64 * (m + 1));
+                if (m < 4) fa[(m + 4) % 5] = frag(at, 128 * wm + 16 * (m + 4) + r);
+            }
+            if (i < 32) t[n] = fp_mfma(fw[n], fa[m % 5]);
+            if (i >= 2) {
+                const int pm = (i - 2) / 4, pn = (i - 2) % 4;
+                const float scale = pm == m || i >= 32 ? f : last;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[pm][pn][k] = __fmaf_rn(scale, t[pn][k], acc[pm][pn][k]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        __builtin_amdgcn_s_setprio(0);
+    };
+    auto half = [&]() __attribute__((always_inline)) {       // the end of a half step
+        __builtin_amdgcn_s_waitcnt(lgkmcnt_zero());
+        asm volatile("s_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto scales = [&](int s) __attribute__((always_inline)) {
+        if ((s & 63) == 0) sw64 = fp_load_wait(wsf + s + lane, cols && s + lane < stages);
+    };
+    if (wm == 0) copy_first(0);
+    else copy_second(0);
+    __builtin_amdgcn_s_waitcnt(vmcnt_at_most(0));
+    asm volatile("s_barrier" ::: "memory");
+    if (wm == 0) {
+        for (int s = 0; s < stages; ++s) {
+            scales(s);
+            copy_first(s + 1);                                  // half step 2 s
+            read(s);
+            half();
+            products(s);                                        // 2 s + 1
+            __builtin_amdgcn_s_waitcnt(vmcnt_at_most(0));
+            half();
+        }
+        half();
+    } else {
+        half();                                                 // half step 0
+        for (int s = 0; s < stages; ++s) {
+            scales(s);
+            copy_second(s + 1);                                 // 2 s + 1
+            read(s);
+            half();
+            products(s);                                        // 2 s + 2
+            __builtin_amdgcn_s_waitcnt(vmcnt_at_most(0));
+            half();
+        }
+    }
+    // the copies of the stages behind the last still write to the LDS
+    __builtin_amdgcn_s_waitcnt(vmcnt_at_most(0) & lgkmcnt_zero());
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+        const int t0 = m0 + 128 * wm + 16 * m;
+        if (t0 < a.T && cols) fp_store<4>(a, lds + wave * 16 * (32 * 4 + 16), acc[m], t0, n0 + 64 * wn, lane);
+    }
+}
+
+template <int MW, int NW, int NB>
 int launch_fp8(const FgArgs& a, hipStream_t s) {
-    using S = FgShape<WM, WN, MW, NW>;
+    using S = FgShape<MW, NW, NB>;
     const int64_t tiles = (int64_t)((a.T + S::kBM - 1) / S::kBM) * ((a.N + S::kBN - 1) / S::kBN);
-    if (!launch_fits(tiles, 64 * S::kWaves)) return fail(MOE_EUNSUPPORTED, "fp8_gemm: too many output tiles");
-    hipLaunchKernelGGL((fp8_gemm_kernel<WM, WN, MW, NW>), dim3((unsigned)tiles), dim3(64 * S::kWaves), 0, s, a);
+    if (!launch_fits(tiles, 256)) return fail(MOE_EUNSUPPORTED, "fp8_gemm: too many output tiles");
+    hipLaunchKernelGGL((fp8_gemm_kernel<MW, NW, NB>), dim3((unsigned)tiles), dim3(256), 0, s, a);
+    return check_launch("fp8_gemm");
+}
+
+static int launch_fp8_wide(const FgArgs& a, hipStream_t s) {
+    const int64_t tiles = (int64_t)((a.T + 255) / 256) * ((a.N + 255) / 256);
+    if (!launch_fits(tiles, 512)) return fail(MOE_EUNSUPPORTED, "fp8_gemm: too many output tiles");
+    hipLaunchKernelGGL(fp8_gemm_wide_kernel, dim3((unsigned)tiles), dim3(512), 0, s, a);
+    return check_launch("fp8_gemm");
+}
+
+template <int TM>
+int launch_fp8_skinny(const FgArgs& a, hipStream_t s) {
+    const int64_t groups = ((int64_t)a.N + 15) / 16;
+    hipLaunchKernelGGL(fp8_gemm_skinny_kernel<TM>, dim3((unsigned)groups), dim3(64 * kFsWaves), 0, s, a);
     return check_launch("fp8_gemm");
 }
 
@@ -412,7 +682,16 @@ extern "C" int fp8_gemm(const uint8_t* a_codes, const float* a_sf, int64_t a_sf_
     if (out_row_stride < N) return fail(MOE_EINVAL, "%s: out row stride %lld must be >= N", name, (long long)out_row_stride);
     FgArgs a{a_codes, a_sf, a_sf_stride, w_codes, w_row_stride, w_sf, T, N, K, out, out_row_stride, out_row_stride % 8 == 0 ? 1 : 0};
     hipStream_t s = (hipStream_t)stream;
-    if (T <= 64) return launch_fp8<1, 4, 1, 1>(a, s);
-    if ((int64_t)T * N >= 2048 * 2048) return launch_fp8<2, 4, 4, 2>(a, s);
-    return launch_fp8<2, 2, 2, 2>(a, s);
+    // us, K = 4096, replayed from a graph: by columns, blocks of 64 x 64, 128 x 128, 256 x 256
+    //   1 x 4096   5.1 11.3 27.3 47.0     16 x 8192  10.4 12.3 27.7 48.1      1 x 16384 13.8 13.7 27.7 48.8
+    //  32 x 4096   8.8 11.9 27.7 48.1     32 x 8192  15.3 12.7 28.0 48.3    512 x 4096    -  15.9 29.2 50.5
+    // 768 x 4096    -  26.1 29.8 51.0   1024 x 4096    -  31.1 30.0 50.6   2048 x 4096    -  60.2 42.3 52.4
+    // 4096 x 4096   -   118 81.5 68.5   8192 x 8192    -   435  299  246
+    // (two of the smaller blocks run on a CU: 512 at once)
+    if (T <= 16 && N <= 8192) return launch_fp8_skinny<1>(a, s);
+    if (T <= 32 && N <= 4096) return launch_fp8_skinny<2>(a, s);
+    const auto tiles = [&](int64_t side) { return (T + side - 1) / side * ((N + side - 1) / side); };
+    if (tiles(64) <= 768) return launch_fp8<2, 2, 2>(a, s);
+    if (tiles(128) <= 512) return launch_fp8<4, 4, 1>(a, s);
+    return launch_fp8_wide(a, s);
 }
