@@ -621,8 +621,10 @@ int moe_combine_bwd(const void* d_out, int64_t d_out_row_stride, const void* row
  *                   (any offsets will do, not multiples of a tile alone)
  * Rows between an expert's last and the next offset (padding) are not read, and
  * are written as zeros where rows are written; rows from the last offset on are
- * neither read nor written. Maps that break these bounds give wrong rows, and
- * never an access outside the rows.
+ * neither read nor written. An offset past rows_max counts as rows_max and a
+ * count past the next offset as the distance to it (so {0, INT32_MAX} and
+ * {INT32_MAX} are one expert of all rows); maps that break these bounds otherwise
+ * give wrong rows, and never an access outside the rows.
  * w device bf16 [E, N, D], contiguous. N and D multiples of 8 up to
  * MOE_MAX_GROUPED; row strides of bf16 operands multiples of 8, at most 2^21.
  * Every sum has a fixed order: results do not change from call to call. One

@@ -29,10 +29,11 @@ __device__ __forceinline__ FpBlock fp_block(uint32_t amax_bits) {
 
 // The quotient from the reciprocal and one correction, the remainder exact (fused
 // multiply-adds). e4m3's ties are 5-bit numbers, and v and m have 8 bits: a quotient
-// is a tie, which the correction gives whole, or 2^-14 away from one.
+// is a tie, which the correction gives whole, or 2^-14 away from one. (It loses a
+// zero's sign: that is v's.)
 __device__ __forceinline__ float fp_quot(float v, const FpBlock& b) {
     const float y = __fmul_rn(v, 0.875f), q = __fmul_rn(y, b.r);
-    return __fmaf_rn(__fmaf_rn(-q, b.d, y), b.r, q);
+    return __builtin_copysignf(__fmaf_rn(__fmaf_rn(-q, b.d, y), b.r, q), v);
 }
 
 __device__ __forceinline__ uint2 fp_codes8(const float (&v)[8], const FpBlock& b) {

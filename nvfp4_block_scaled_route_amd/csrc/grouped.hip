@@ -523,7 +523,7 @@ static int gg_rows_call(const uint16_t* x, int64_t x_row_stride, const uint16_t*
     if (rc != MOE_OK) return rc;
     if (!out || (in_cols && (!x || !w))) return fail(MOE_EINVAL, "%s: NULL pointer", name);
     if (!aligned16(x) || !aligned16(w) || !aligned16(out)) return fail(MOE_EINVAL, "%s: pointers must be 16-byte aligned", name);
-    if (gg_bad_stride(x_row_stride, in_cols) || out_row_stride < out_cols)
+    if ((in_cols && gg_bad_stride(x_row_stride, in_cols)) || out_row_stride < out_cols)
         return fail(MOE_EINVAL, "%s: row strides must be >= the rows (the input's a multiple of 8, at most %d)", name, 1 << 21);
     GgArgs a{};
     a.a = (const uint8_t*)x; a.a_stride = 2 * x_row_stride;

@@ -51,8 +51,16 @@ struct SgUnit {
     }
 };
 
-// 1 + exp(-g) overflows to infinity for g < -88.7, where s is 0 to fp32.
-__device__ __forceinline__ float sg_sigmoid(float g) { return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-g))); }
+// s = 1 / (1 + exp(-g)) and 1 - s, either without overflow or cancellation: with
+// t = exp(-|g|) the larger is 1 / (1 + t) and the smaller t / (1 + t).
+struct Sigmoid {
+    float s, rest;
+    __device__ __forceinline__ explicit Sigmoid(float g) {
+        const float t = expf(-__builtin_fabsf(g)), large = __fdiv_rn(1.0f, __fadd_rn(1.0f, t)), small = __fmul_rn(t, large);
+        s = g < 0.0f ? small : large;
+        rest = g < 0.0f ? large : small;
+    }
+};
 
 template <bool kF32, bool kBwd>
 __global__ void __launch_bounds__(kSgThreads) swiglu_kernel(SgArgs a) {
@@ -77,15 +85,16 @@ __global__ void __launch_bounds__(kSgThreads) swiglu_kernel(SgArgs a) {
     SgUnit<kF32>::load(in + half, u);
     if constexpr (!kBwd) {
 #pragma unroll
-        for (int i = 0; i < n; ++i) y[i] = __fmul_rn(__fmul_rn(g[i], sg_sigmoid(g[i])), u[i]);
+        for (int i = 0; i < n; ++i) y[i] = __fmul_rn(__fmul_rn(g[i], Sigmoid(g[i]).s), u[i]);
         SgUnit<kF32>::store(out, y);
     } else {
         SgUnit<kF32>::load(a.d_inter + row * a.d_inter_stride + at, y);
 #pragma unroll
         for (int i = 0; i < n; ++i) {
-            const float s = sg_sigmoid(g[i]), silu = __fmul_rn(g[i], s);
+            const Sigmoid z(g[i]);
+            const float silu = __fmul_rn(g[i], z.s);
             // s (1 + g (1 - s)) = s + silu (1 - s)
-            const float d_g = __fmul_rn(__fmul_rn(y[i], u[i]), __fmaf_rn(silu, __fsub_rn(1.0f, s), s));
+            const float d_g = __fmul_rn(__fmul_rn(y[i], u[i]), __fmaf_rn(silu, z.rest, z.s));
             u[i] = __fmul_rn(y[i], silu);
             g[i] = d_g;
         }

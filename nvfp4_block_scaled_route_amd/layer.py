@@ -4,8 +4,9 @@ The step order is the model page's "_prepared_nvfp4_forward" and the runner
 page's "MuseSparkTrtLlmNvFp4Experts.apply_routed" / "MusePostExpertFinalize":
 route, quantize the expert input, experts up to the GEMM2 rows, finalize. This
 module only allocates device buffers (torch) and calls the library; all
-arithmetic runs in the HIP kernels. MxLinear is a dense projection in front of
-or behind that path.
+arithmetic runs in the HIP kernels. MxLinear and Fp8Linear are dense projections
+in front of or behind that path, Routing and ExpertMlp bf16 experts that are
+trained.
 
 Expert TP on one GPU (the expert_tp page): the tp slices of the converted
 weights are byte views (``slice_weights``); each slice's experts write their
@@ -60,6 +61,17 @@ def slice_weights(full: N.Weights, r: int, tp: int, H: int, I: int) -> N.Weights
         w2_offset=full.w2_offset + t2 * 1024, w2_sf_offset=full.w2_sf_offset + t2 * 128)
 
 
+def _owner(stream):
+    """The context in which buffers that `stream` owns are allocated: memory that
+    another stream freed may still be written by the work in front of the free.
+    None: the current stream."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
 class MxLinear:
     """A dense projection around the experts (the model page, "MuseSpark1xMoE":
     the pooler and unpooler) in MX formats: out = x times weight transposed, the
@@ -107,6 +119,151 @@ class MxLinear:
         codes, sf = self._rows(x)
         N.mx_add_norm_quant(x, residual, norm_weight, gain_center, eps, self.a_fmt, sum_out, codes, sf, stream)
         N.mx_gemm(codes, sf, self.a_fmt, self.w_codes, self.w_sf, self.w_fmt, out, stream)
+
+
+class Fp8Linear:
+    """A dense projection in e4m3 with one fp32 scale for each block of 128: out =
+    x times weight transposed, the weight [N, K] (bf16, K a multiple of 16) quantized
+    by load(), x per call. input_grad and weight_grad are its gradients: the former in
+    the same format on the transposed weight (with grads=True; N a multiple of 16),
+    the latter in bf16 on x and d_out themselves (N and K multiples of 8). Holds the
+    buffers of calls with up to max_tokens rows; streams, captures and the life of
+    the buffers are as with MxLinear."""
+
+    def __init__(self, weight_bf16, max_tokens: int, grads: bool = False, stream=None):
+        n, k = weight_bf16.shape
+        N.fp8_gemm_validate(n, k)       # here, not at the first call
+        if grads:
+            N.fp8_gemm_validate(k, n)
+        self.N, self.K, self.max_tokens, self.grads = n, k, max_tokens, grads
+        dev = weight_bf16.device
+
+        def blocks(rows):
+            return (rows + 127) // 128
+
+        with _owner(stream):
+            self.w_codes = torch.empty((n, k), dtype=torch.uint8, device=dev)
+            self.w_sf = torch.empty((blocks(n), blocks(k)), dtype=torch.float32, device=dev)
+            self.wt_codes = torch.empty((k, n), dtype=torch.uint8, device=dev) if grads else None
+            self.wt_sf = torch.empty((blocks(k), blocks(n)), dtype=torch.float32, device=dev) if grads else None
+            widest = max(n, k) if grads else k
+            self.a_codes = torch.empty((max_tokens * widest,), dtype=torch.uint8, device=dev)
+            self.a_sf = torch.empty((blocks(widest) * max_tokens,), dtype=torch.float32, device=dev)
+            # one expert of all rows there are
+            self.all_rows = torch.full((1,), 0x7FFFFFFF, dtype=torch.int32, device=dev)
+            self.from_first = torch.cat((torch.zeros_like(self.all_rows), self.all_rows))
+        self.load(weight_bf16, stream)
+
+    def load(self, weight_bf16, stream=None) -> None:
+        """Quantizes the weight (again, after a step of the optimizer)."""
+        if tuple(weight_bf16.shape) != (self.N, self.K):
+            raise ValueError(f"a weight of {tuple(weight_bf16.shape)}, not {(self.N, self.K)}")
+        N.fp8_quant_weight(weight_bf16, self.w_codes, self.w_sf, self.wt_codes, self.wt_sf, stream)
+        if stream is not None:      # the caller may drop the weight while that stream still reads it
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+            weight_bf16.record_stream(stream)
+
+    def _product(self, x, w_codes, w_sf, out, stream):
+        T, K = x.shape
+        if T > self.max_tokens:
+            raise ValueError(f"{T} tokens, more than the {self.max_tokens} this projection was made for")
+        if K != w_codes.shape[1]:
+            raise ValueError(f"rows of {K} values, not {w_codes.shape[1]}")
+        codes, sf = self.a_codes[:T * K].view(T, K), self.a_sf[:(K + 127) // 128 * T].view(-1, T)
+        N.fp8_quant(x, codes, sf, stream)
+        N.fp8_gemm(codes, sf, w_codes, w_sf, out, stream)
+
+    def __call__(self, x, out, stream=None) -> None:
+        """out bf16 [T, N] = x [T, K] times the weight transposed."""
+        self._product(x, self.w_codes, self.w_sf, out, stream)
+
+    def input_grad(self, d_out, d_x, stream=None) -> None:
+        """d_x bf16 [T, K] = d_out [T, N] times the weight."""
+        if not self.grads:
+            raise ValueError("this projection was made without grads")
+        self._product(d_out, self.wt_codes, self.wt_sf, d_x, stream)
+
+    def weight_grad(self, d_out, x, d_w, accumulate: bool = False, stream=None) -> None:
+        """d_w [N, K] (bf16 or fp32) = d_out transposed times x, or that added to it."""
+        N.moe_grouped_gemm_wgrad(d_out, x, self.from_first, self.all_rows, d_w.unsqueeze(0), accumulate, stream)
+
+
+class Routing:
+    """A routing of T tokens to K of E experts: what moe_route writes, and its fields
+    as the calls on sorted rows take them."""
+
+    def __init__(self, T: int, K: int, E: int, tile_m: int, device="cuda"):
+        self.T, self.K, self.E, self.tile_m = T, K, E, tile_m
+        self.layout = N.moe_meta_layout_get(T, K, E, tile_m)
+        self.meta = torch.full((self.layout.total_ints,), -1, dtype=torch.int32, device=device)
+        self.ids = torch.empty((T, K), dtype=torch.int32, device=device)
+        self.weights = torch.empty((T, K), dtype=torch.float32, device=device)
+        L = self.layout
+
+        def field(at, length):
+            return self.meta[at:at + length]
+
+        self.exp2perm = field(L.exp2perm, T * K).view(T, K)
+        self.perm2tok = field(L.perm2tok, L.rows_max)
+        self.total_rows = field(L.total_rows, 1)
+        self.expert_offsets = field(L.expert_offsets, E + 1)
+        self.expert_counts = field(L.expert_counts, E)
+
+    def __call__(self, logits, expert_bias=None, is_padding=None, route_scale: float = 1.0, stream=None) -> None:
+        N.moe_route(logits, expert_bias, is_padding, self.K, route_scale, self.tile_m, 0, self.E, self.ids, self.weights,
+                    self.meta, stream)
+
+
+class ExpertMlp:
+    """bf16 experts that are trained, out[t] = sum over t's routes of weight * w2[e]
+    (silu(g) * u), (g, u) = w13[e] x[t]: the tokens sorted by expert, the two products
+    grouped by expert with the gated activation between them, and back with the
+    routes' weights (moe_experts_fwd_bf16 with moe_finalize is the serving form, and
+    norms each row). w13 bf16 [E, 2 I, H], gate rows first, w2 bf16 [E, H, I].
+
+    forward keeps what backward needs in this object's buffers, and backward uses
+    them up: a backward belongs to the last forward, on the same routing, and calls
+    that share one ExpertMlp must not overlap. Nothing is allocated per call, so
+    they can be captured."""
+
+    def __init__(self, T: int, K: int, E: int, H: int, I: int, tile_m: int, device="cuda"):
+        self.T, self.K, self.E, self.H, self.I = T, K, E, H, I
+        R = self.R = N.moe_rows_max(T, K, E, tile_m)
+
+        def rows(width):
+            return torch.empty((R, width), dtype=torch.bfloat16, device=device)
+
+        self.rows, self.gate_up, self.inter, self.out_rows = rows(H), rows(2 * I), rows(I), rows(H)
+        self.d_inter, self.d_rows = rows(I), rows(H)
+        self._kept = False
+
+    def forward(self, x, routing: Routing, w13, w2, out, stream=None) -> None:
+        """out bf16 [T, H]."""
+        r = routing
+        N.moe_dispatch(x, r.exp2perm, r.perm2tok, r.total_rows, self.rows, stream)
+        N.moe_grouped_gemm(self.rows, w13, r.expert_offsets, r.expert_counts, self.gate_up, stream)
+        N.moe_swiglu(self.gate_up, r.perm2tok, r.total_rows, self.inter, stream)
+        N.moe_grouped_gemm(self.inter, w2, r.expert_offsets, r.expert_counts, self.out_rows, stream)
+        N.moe_combine(self.out_rows, r.exp2perm, r.weights, out, stream)
+        self._kept = True
+
+    def backward(self, d_out, routing: Routing, w13, w2, d_x, d_w13, d_w2, d_weights, accumulate: bool = False,
+                 stream=None) -> None:
+        """From d_out bf16 [T, H]: d_x bf16 [T, H], d_w13 and d_w2 (bf16 or fp32, added to
+        with accumulate) and d_weights fp32 [T, K]."""
+        if not self._kept:
+            raise ValueError("a backward without its forward")
+        self._kept = False
+        r = routing
+        d_rows2, d_gate_up = self.out_rows, self.gate_up        # in place
+        N.moe_combine_bwd(d_out, self.out_rows, r.exp2perm, r.perm2tok, r.total_rows, r.weights, d_rows2, d_weights, stream)
+        N.moe_grouped_gemm_wgrad(d_rows2, self.inter, r.expert_offsets, r.expert_counts, d_w2, accumulate, stream)
+        N.moe_grouped_gemm_dgrad(d_rows2, w2, r.expert_offsets, r.expert_counts, self.d_inter, stream)
+        N.moe_swiglu_bwd(self.d_inter, self.gate_up, r.perm2tok, r.total_rows, d_gate_up, stream)
+        N.moe_grouped_gemm_wgrad(d_gate_up, self.rows, r.expert_offsets, r.expert_counts, d_w13, accumulate, stream)
+        N.moe_grouped_gemm_dgrad(d_gate_up, w13, r.expert_offsets, r.expert_counts, self.d_rows, stream)
+        N.moe_dispatch_bwd(self.d_rows, r.exp2perm, d_x, stream)
 
 
 @dataclass

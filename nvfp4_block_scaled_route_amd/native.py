@@ -691,3 +691,11 @@ def fp8_gemm(a_codes, a_sf, w_codes, w_sf, out, stream=None) -> None:
                         _flat(call, "w_sf", w_sf, _F32, (_blocks(N), _blocks(K)), dev), T, N, K, out.data_ptr(), ld, st)
     if rc:
         _check(rc, call)
+
+
+def fp8_gemm_validate(N, K) -> None:
+    """Host-only check that fp8_gemm takes these sizes; raises MoeError. (A call of no
+    tokens: it checks them, reads nothing and launches nothing.)"""
+    if N > _I32_MAX or K > _I32_MAX:
+        raise MoeError(f"fp8_gemm: N={N} or K={K} is too large")
+    _check(lib().fp8_gemm(None, None, 0, None, K, None, 0, N, K, None, N, None), "fp8_gemm")

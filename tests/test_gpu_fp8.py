@@ -1,0 +1,241 @@
+"""e4m3 with a scale for each block of 128: the quantizers bit for bit, the product
+within bounds derived from its roundings."""
+import numpy as np
+import pytest
+import torch
+
+from nvfp4_block_scaled_route_amd import native as N
+from oracle import formats as F
+from oracle import fp8 as Q
+
+from .gpu_common import DEV, dev, host, say
+
+pytestmark = pytest.mark.gpu
+
+
+def _bits(rng, T, H, scale=1.0):
+    x = rng.standard_normal((T, H)) * scale
+    return F.f32_to_bf16(np.where(rng.random((T, H)) < 0.01, 20 * x, x).astype(np.float32))
+
+
+def _padded(bits, pad):
+    wide = np.full((bits.shape[0], bits.shape[1] + pad), 0x7FC0, np.uint16)
+    wide[:, :bits.shape[1]] = bits
+    return dev(wide)[:, :bits.shape[1]]
+
+
+def _same(codes, sf, bits, tall):
+    want, scales = Q.quantize(F.bf16_to_f64(bits), tall)
+    assert np.array_equal(sf.view(np.uint32) & 0x7FFFFFFF, scales.view(np.uint32) & 0x7FFFFFFF)
+    assert np.array_equal(codes, want), np.argwhere(codes != want)[:4]
+
+
+def _quant(bits, pad=0, sf_pad=0):
+    T, H = bits.shape
+    codes = torch.full((T, H), 0xAB, dtype=torch.uint8, device=DEV)
+    wide = torch.full((Q.blocks(H), T + sf_pad), -3.0, device=DEV)
+    say(f"fp8_quant T={T} H={H} pad={pad},{sf_pad}")
+    N.fp8_quant(_padded(bits, pad), codes, wide[:, :T])
+    torch.cuda.synchronize()
+    assert (wide[:, T:] == -3.0).all()
+    _same(host(codes), np.ascontiguousarray(wide[:, :T].t().cpu().numpy()), bits, 1)
+
+
+def _quant_weight(bits, pad=0, t_pad=None):
+    n, k = bits.shape
+    codes = torch.full((n, k), 0xAB, dtype=torch.uint8, device=DEV)
+    sf = torch.full((Q.blocks(n), Q.blocks(k)), -3.0, device=DEV)
+    wide = (n + 15) // 16 * 16 + (t_pad or 0)
+    ct = torch.full((k, wide), 0xCD, dtype=torch.uint8, device=DEV)
+    st = torch.full((Q.blocks(k), Q.blocks(n)), -3.0, device=DEV)
+    say(f"fp8_quant_weight N={n} K={k} pad={pad} transposed={t_pad}")
+    if t_pad is None:
+        N.fp8_quant_weight(_padded(bits, pad), codes, sf)
+    else:
+        N.fp8_quant_weight(_padded(bits, pad), codes, sf, ct[:, :n], st)
+    torch.cuda.synchronize()
+    _same(host(codes), sf.cpu().numpy(), bits, 128)
+    if t_pad is not None:
+        assert torch.equal(ct[:, :n], codes.t()) and (ct[:, n:] == 0xCD).all()
+        assert np.array_equal(st.cpu().numpy().view(np.uint32), np.ascontiguousarray(sf.cpu().numpy().T).view(np.uint32))
+
+
+@pytest.mark.parametrize("T,H,pad,sf_pad", [(1, 16, 0, 0), (1, 128, 8, 0), (3, 144, 0, 5), (16, 256, 0, 0), (17, 4096, 0, 0),
+                                            (300, 1040, 24, 1), (5, 16384, 0, 3), (1000, 16, 8, 0)])
+def test_quant_shapes(T, H, pad, sf_pad):
+    _quant(_bits(np.random.default_rng(T + H), T, H), pad, sf_pad)
+
+
+@pytest.mark.parametrize("n,k,pad,t_pad", [(1, 16, 0, 0), (128, 128, 0, None), (130, 144, 8, 16), (257, 400, 0, 0), (15, 16, 0, 0),
+                                           (1000, 272, 16, 32), (384, 4096, 0, None)])
+def test_quant_weight_shapes(n, k, pad, t_pad):
+    _quant_weight(_bits(np.random.default_rng(n + k), n, k, 0.03), pad, t_pad)
+
+
+def test_quant_every_bf16_value():
+    """All 65536 bit patterns, each beside a block maximum of each of several sizes
+    (below and at the least one, where 448 / m is whole and where it is not, NaN and
+    infinity)."""
+    bits = np.arange(65536, dtype=np.uint16)
+    for top in (0x0001, 0x0080, 0x0D80, 0x0D81, 0x3F80, 0x3FE0, 0x40E0, 0x4123, 0x7F7F, 0x7F80):
+        rows = np.resize(bits, (517, 127))
+        small = (rows & 0x7FFF) <= (top & 0x7FFF)       # values that leave the maximum where it is, too
+        _quant(np.concatenate([np.full((517, 1), top, np.uint16), rows], axis=1))
+        _quant(np.concatenate([np.full((517, 1), top, np.uint16), np.where(small, rows, 0).astype(np.uint16)], axis=1))
+
+
+def test_quant_blocks_with_nothing_finite():
+    """Zeros (of both signs), NaN or infinity in a block: that block alone."""
+    x = np.zeros((4, 384), np.float32)
+    x[1, 130], x[2, 0], x[3, 383] = np.nan, np.inf, -0.0
+    x[1, :128] = 1.0
+    _quant(F.f32_to_bf16(x))
+    _quant_weight(F.f32_to_bf16(x), 0, 0)
+
+
+# ------------------------------------------------------------------ product
+def _operands(rng, T, Nn, K, w_pad=0):
+    """Codes and scales of random values whose rows and blocks differ in size."""
+    a = F.bf16_to_f64(_bits(rng, T, K)) * np.exp2(rng.integers(-6, 7, (T, 1)))
+    w = F.bf16_to_f64(_bits(rng, Nn, K, K ** -0.5)) * np.exp2(rng.integers(-3, 4, (Nn, 1)))
+    ac, asf = Q.quantize(F.bf16_to_f64(F.f32_to_bf16(a.astype(np.float32))), 1)
+    wc, wsf = Q.quantize(F.bf16_to_f64(F.f32_to_bf16(w.astype(np.float32))), 128)
+    wide = np.full((Nn, K + w_pad), 0x7F, np.uint8)      # NaN codes behind the rows
+    wide[:, :K] = wc
+    return (ac, asf, wc, wsf), (dev(ac), dev(np.ascontiguousarray(asf.T)), dev(wide)[:, :K], dev(wsf))
+
+
+def _bound(av, wv, ref, mags, tops, K):
+    """Inside a block each group of 8 products is cut at 2^-13 of the largest one's
+    exponent: at most 8 * 2^-13 of the product of the operands' largest; a block's 16
+    groups are added in at most 4 levels, each off by 2^-23; the scales' product and the
+    sum onto the accumulator by 2^-24 of theirs, K / 128 times, and the waves' sums (8
+    joins). Then half a bf16 step."""
+    err = 2.0 ** -10 * tops + (4 + 1 + K / 128 + 8) * 2.0 ** -23 * mags
+    return err + 2.0 ** -8 * (np.abs(ref) + err) + 2.0 ** -134
+
+
+def _product(T, Nn, K, w_pad=0, out_pad=0, seed=0):
+    rng = np.random.default_rng(seed + T + Nn + K)
+    (ac, asf, wc, wsf), t = _operands(rng, T, Nn, K, w_pad)
+    wide = torch.full((T, Nn + out_pad), 0x4141, dtype=torch.int16, device=DEV)
+    say(f"fp8_gemm T={T} N={Nn} K={K} pad={w_pad},{out_pad}")
+    N.fp8_gemm(*t, wide[:, :Nn])
+    torch.cuda.synchronize()
+    av, wv = Q.values(ac, asf, 1), Q.values(wc, wsf, 128)
+    ref, mags, tops = Q.gemm(av, wv)
+    got = F.bf16_to_f64(host(wide))
+    bad = ~(np.abs(got[:, :Nn] - ref) <= _bound(av, wv, ref, mags, tops, K))
+    assert not bad.any(), f"{int(bad.sum())} values, first at {np.argwhere(bad)[0]}"
+    assert (host(wide)[:, Nn:] == 0x4141).all()
+
+
+@pytest.mark.parametrize("T,Nn,K", [(1, 1, 16), (1, 4096, 4096), (2, 17, 144), (15, 130, 1040), (16, 16, 128), (17, 300, 2064),
+                                    (32, 4096, 400), (9, 1000, 5120), (3, 8192, 16)])
+def test_few_tokens(T, Nn, K):
+    _product(T, Nn, K)
+
+
+@pytest.mark.parametrize("T,Nn,K", [(33, 1, 16), (33, 64, 128), (64, 65, 256), (65, 130, 272), (517, 2085, 400), (130, 70, 4112),
+                                    (1, 8200, 144), (32, 4112, 1024), (100, 64, 8192), (63, 129, 8208)])
+def test_blocks_of_64(T, Nn, K):
+    _product(T, Nn, K)
+
+
+@pytest.mark.parametrize("T,Nn,K", [(1100, 3000, 144), (2000, 2100, 272), (1025, 4000, 128), (2048, 3999, 16)])
+def test_blocks_of_128(T, Nn, K):
+    _product(T, Nn, K)
+
+
+@pytest.mark.parametrize("T,Nn,K", [(3000, 4000, 144), (2900, 4100, 16), (4095, 3001, 400), (257, 40000, 128), (2900, 3900, 8208)])
+def test_blocks_of_256(T, Nn, K):
+    _product(T, Nn, K)
+
+
+@pytest.mark.parametrize("T,Nn,K", [(5, 40, 144), (70, 100, 272), (1100, 3000, 144), (3000, 4001, 272)])
+def test_strides(T, Nn, K):
+    _product(T, Nn, K, w_pad=48, out_pad=3)
+    _product(T, Nn, K, w_pad=16, out_pad=8)
+
+
+@pytest.mark.parametrize("T,Nn", [(9, 200), (70, 300), (1100, 3000), (3000, 4000)])
+def test_nan_scales_and_codes_stay_in_their_rows_and_columns(T, Nn):
+    K = 400
+    _, (ac, asf, wc, wsf) = _operands(np.random.default_rng(T), T, Nn, K)
+    out = torch.empty((T, Nn), dtype=torch.bfloat16, device=DEV)
+    asf[1, 3] = float("nan")
+    ac[7, 399] = 0x7F
+    wc[150, 0] = 0xFF
+    wsf[0, 2] = float("nan")
+    say(f"fp8_gemm with NaN T={T} N={Nn}")
+    N.fp8_gemm(ac, asf, wc, wsf, out)
+    torch.cuda.synchronize()
+    bad = ~np.isfinite(out.float().cpu().numpy())
+    want = np.zeros_like(bad)
+    want[[3, 7]] = True
+    want[:, 150] = want[:, :128] = True
+    assert np.array_equal(bad, want)
+
+
+def test_scale_rows_longer_than_the_tokens():
+    """A batch of fewer tokens in the buffers of a larger one."""
+    T, Nn, K = 40, 100, 272
+    (ac, asf, wc, wsf), t = _operands(np.random.default_rng(1), T, Nn, K)
+    wide = torch.full((Q.blocks(K), 100), float("nan"), device=DEV)
+    wide[:, :T] = t[1]
+    first, out = (torch.empty((T, Nn), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    N.fp8_gemm(*t, first)
+    N.fp8_gemm(t[0], wide[:, :T], t[2], t[3], out)
+    torch.cuda.synchronize()
+    assert torch.equal(first, out)
+
+
+@pytest.mark.parametrize("T,Nn", [(16, 500), (70, 500), (1100, 3000), (3000, 4000)])
+def test_same_bits_from_call_to_call(T, Nn):
+    _, t = _operands(np.random.default_rng(T), T, Nn, 528)
+    outs = [torch.empty((T, Nn), dtype=torch.bfloat16, device=DEV) for _ in range(4)]
+    for o in outs:
+        N.fp8_gemm(*t, o)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, outs[0]) for o in outs)
+
+
+def test_past_32_bits():
+    """A weight of more than 2^32 bytes and its quantizer, a batch of more."""
+    n, k = 70000, 65536
+    w = torch.zeros((n, k), dtype=torch.bfloat16, device=DEV)
+    w[-200:] = torch.randn(200, k, device=DEV).bfloat16()
+    codes = torch.empty((n, k), dtype=torch.uint8, device=DEV)
+    sf = torch.empty((Q.blocks(n), Q.blocks(k)), device=DEV)
+    say("past 32 bits: weight")
+    N.fp8_quant_weight(w, codes, sf)
+    x = torch.randn(3, k, device=DEV).bfloat16()
+    xc, xs = torch.empty((3, k), dtype=torch.uint8, device=DEV), torch.empty((Q.blocks(k), 3), device=DEV)
+    N.fp8_quant(x, xc, xs)
+    out = torch.empty((3, n), dtype=torch.bfloat16, device=DEV)
+    N.fp8_gemm(xc, xs, codes, sf, out)
+    torch.cuda.synchronize()
+    lo = n - 200 - (n - 200) % 128      # whole blocks of rows
+    bits = host(w[lo:].view(torch.int16))
+    wc, wsf = Q.quantize(F.bf16_to_f64(bits), 128)
+    assert np.array_equal(host(codes[lo:]), wc) and np.array_equal(sf[lo // 128:].cpu().numpy(), wsf)
+    av, wv = Q.values(host(xc), np.ascontiguousarray(xs.t().cpu().numpy()), 1), Q.values(wc, wsf, 128)
+    ref, mags, tops = Q.gemm(av, wv)
+    got = out[:, lo:].double().cpu().numpy()
+    assert (np.abs(got - ref) <= _bound(av, wv, ref, mags, tops, k)).all()
+    assert (out[:, :lo] == 0).all()
+    say("past 32 bits: tokens")
+    sf = torch.empty((Q.blocks(k), n), device=DEV)
+    N.fp8_quant(w, codes, sf)
+    torch.cuda.synchronize()
+    wc, wsf = Q.quantize(F.bf16_to_f64(bits), 1)
+    assert np.array_equal(host(codes[lo:]), wc) and np.array_equal(sf[:, lo:].t().cpu().numpy(), wsf)
+    small = torch.randn(16, k, device=DEV).bfloat16()
+    sc, ss = torch.empty((16, k), dtype=torch.uint8, device=DEV), torch.empty((1, Q.blocks(k)), device=DEV)
+    N.fp8_quant_weight(small, sc, ss)
+    out = torch.empty((n, 16), dtype=torch.bfloat16, device=DEV)
+    N.fp8_gemm(codes, sf, sc, ss, out)
+    torch.cuda.synchronize()
+    av, wv = Q.values(wc, wsf, 1), Q.values(host(sc), ss.cpu().numpy(), 128)
+    ref, mags, tops = Q.gemm(av, wv)
+    assert (np.abs(out[lo:].double().cpu().numpy() - ref) <= _bound(av, wv, ref, mags, tops, k)).all()
