@@ -10,8 +10,11 @@
  * A layer runs, on one stream, in this order:
  *   moe_route -> nvfp4_quant -> moe_experts_fwd -> moe_finalize
  * (moe_route_quant is the first two in one launch); beside it stand dense
- * products in MX formats (mx_*) and the sort of tokens by expert and back
- * (moe_dispatch, moe_combine), with the gradients
+ * products in MX formats (mx_*) and in e4m3 with a scale for each block of 128
+ * (fp8_*), the sort of tokens by expert and back (moe_dispatch, moe_combine), and
+ * what stands between the two for experts that are trained, products grouped by
+ * expert and the gated activation (moe_grouped_gemm, moe_swiglu), the sort and these
+ * with their gradients
  * (the model page, "_prepared_nvfp4_forward", prepares the quantized input and
  * the routing; the runner page, "MuseSparkTrtLlmNvFp4Experts.apply_routed", runs
  * the experts up to the GEMM2 rows and hands them to "MusePostExpertFinalize").
@@ -57,6 +60,7 @@ extern "C" {
 #define MOE_MAX_TOPK 32
 #define MOE_MAX_HIDDEN 16384  /* H, and I in moe_experts_fwd */
 #define MOE_MAX_GROUPED 32768 /* N and D of moe_grouped_gemm */
+#define MOE_MAX_ROWS 0x7FFFF000 /* rows of the products by expert, either side of the 8-bit ones */
 
 int moe_abi_version(void);
 const char* moe_last_error(void);
@@ -625,8 +629,8 @@ int moe_combine_bwd(const void* d_out, int64_t d_out_row_stride, const void* row
  * count past the next offset as the distance to it (so {0, INT32_MAX} and
  * {INT32_MAX} are one expert of all rows); maps that break these bounds otherwise
  * give wrong rows, and never an access outside the rows.
- * w device bf16 [E, N, D], contiguous. N and D multiples of 8 up to
- * MOE_MAX_GROUPED; row strides of bf16 operands multiples of 8, at most 2^21.
+ * w device bf16 [E, N, D], contiguous. rows_max up to MOE_MAX_ROWS, N and D
+ * multiples of 8 up to MOE_MAX_GROUPED; row strides of bf16 operands multiples of 8, at most 2^21.
  * Every sum has a fixed order: results do not change from call to call. One
  * launch each, no workspace.
  *
@@ -680,6 +684,7 @@ int moe_swiglu_bwd(const void* d_inter, int64_t d_inter_row_stride, const void* 
  * Of a block with largest magnitude m (at least 2^-100):
  *   sf = m / 448;  code_i = e4m3(v_i * 448 / m)    one rounding each, ties to the even code
  *   any NaN or infinity in the block: sf NaN, codes 0
+ * T and H, N and K, T and N of the three are at most MOE_MAX_ROWS.
  *
  * fp8_quant: activations.
  *   x      device bf16 [T, H], row stride x_row_stride elements (>= H, % 8 == 0)
@@ -708,8 +713,10 @@ int fp8_quant_weight(const uint16_t* w, int64_t w_row_stride, int N, int K, uint
  *            [ceil(N/128), ceil(K/128)], contiguous
  *   out      device bf16 [T, N], row stride out_row_stride elements (>= N)
  * Inside a block the matrix cores cut each product to 13 bits below the exponent of the
- * largest of its 8, as in mx_gemm. A NaN scale or code makes the row or the column NaN.
- * K % 16 == 0, 16 <= K <= MOE_MAX_MX_K; any T and N. One launch, no workspace. */
+ * largest of its 8, as in mx_gemm. The two scales are multiplied first: where their
+ * product leaves fp32's range (below 2^-126 it loses bits, past 2^128 it is infinite) so
+ * does the result. A NaN scale or code makes the row or the column NaN.
+ * K % 16 == 0, 16 <= K <= MOE_MAX_MX_K. One launch, no workspace. */
 int fp8_gemm(const uint8_t* a_codes, const float* a_sf, int64_t a_sf_stride, const uint8_t* w_codes, int64_t w_row_stride,
              const float* w_sf, int T, int N, int K, uint16_t* out, int64_t out_row_stride, void* stream);
 

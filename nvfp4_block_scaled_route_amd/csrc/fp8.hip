@@ -58,6 +58,12 @@ __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
     return v > b ? v : b;
 }
 
+// Sizes behind whose last row or column a block of 256 stays in 31 bits.
+static int fp_sizes(int rows, int cols, const char* name) {
+    return rows <= MOE_MAX_ROWS && cols <= MOE_MAX_ROWS ? MOE_OK
+                                                        : fail(MOE_EUNSUPPORTED, "%s: %d x %d: a side is more than %d", name, rows, cols, MOE_MAX_ROWS);
+}
+
 struct FqArgs {
     const uint16_t* x;
     int64_t x_row_stride;
@@ -630,7 +636,8 @@ extern "C" int fp8_quant(const uint16_t* x, int64_t x_row_stride, int T, int H, 
     const char* name = "fp8_quant";
     if (T < 0 || H < 0) return fail(MOE_EINVAL, "%s: negative size T=%d H=%d", name, T, H);
     if (H % 16) return fail(MOE_EUNSUPPORTED, "%s: H=%d is not a multiple of 16", name, H);
-    if (T == 0 || H == 0) return MOE_OK;
+    const int rc = fp_sizes(T, H, name);
+    if (rc != MOE_OK || T == 0 || H == 0) return rc;
     if (!x || !codes || !sf) return fail(MOE_EINVAL, "%s: NULL pointer", name);
     if (!aligned16(x) || !aligned16(codes) || !aligned16(sf)) return fail(MOE_EINVAL, "%s: pointers must be 16-byte aligned", name);
     if (x_row_stride < H || x_row_stride % 8)
@@ -649,7 +656,8 @@ extern "C" int fp8_quant_weight(const uint16_t* w, int64_t w_row_stride, int N, 
     const char* name = "fp8_quant_weight";
     if (N < 0 || K < 0) return fail(MOE_EINVAL, "%s: negative size N=%d K=%d", name, N, K);
     if (K % 16) return fail(MOE_EUNSUPPORTED, "%s: K=%d is not a multiple of 16", name, K);
-    if (N == 0 || K == 0) return MOE_OK;
+    const int rc = fp_sizes(N, K, name);
+    if (rc != MOE_OK || N == 0 || K == 0) return rc;
     if (!w || !codes || !sf) return fail(MOE_EINVAL, "%s: NULL pointer", name);
     if (!codes_t != !sf_t) return fail(MOE_EINVAL, "%s: transposed codes and scales go together", name);
     if (!aligned16(w) || !aligned16(codes) || !aligned16(sf) || !aligned16(codes_t) || !aligned16(sf_t))
@@ -672,7 +680,8 @@ extern "C" int fp8_gemm(const uint8_t* a_codes, const float* a_sf, int64_t a_sf_
     if (T < 0 || N < 0 || K < 0) return fail(MOE_EINVAL, "%s: negative size T=%d N=%d K=%d", name, T, N, K);
     if (K < 16 || K % 16 || K > MOE_MAX_MX_K)
         return fail(MOE_EUNSUPPORTED, "%s: K=%d must be a multiple of 16 in [16, %d]", name, K, MOE_MAX_MX_K);
-    if (T == 0 || N == 0) return MOE_OK;
+    const int rc = fp_sizes(T, N, name);
+    if (rc != MOE_OK || T == 0 || N == 0) return rc;
     if (!a_codes || !a_sf || !w_codes || !w_sf || !out) return fail(MOE_EINVAL, "%s: NULL pointer", name);
     if (!aligned16(a_codes) || !aligned16(a_sf) || !aligned16(w_codes) || !aligned16(w_sf) || !aligned16(out))
         return fail(MOE_EINVAL, "%s: pointers must be 16-byte aligned", name);

@@ -253,18 +253,10 @@ __device__ __forceinline__ void gg_store(uint8_t* out, int64_t stride, bool vec,
             u32x4 old = {};
             if constexpr (ADD) old = *reinterpret_cast<const u32x4*>(dst);
             *reinterpret_cast<u32x4*>(dst) = piece(src, old);
-        } else {        // (accumulating outputs are contiguous, their rows whole pieces but for a bf16 row's or fp32 row's own end)
+        } else if constexpr (!ADD) {        // rows at any stride; d_w's are contiguous, whole pieces
             for (int k = 0; k < kPiece && c + k < cols; ++k) {
-                float v = kWide ? reinterpret_cast<const float*>(src)[k] : 0.0f;
-                if constexpr (F32) {
-                    float* d = reinterpret_cast<float*>(dst) + k;
-                    *d = ADD ? __fadd_rn(v, *d) : v;
-                } else if constexpr (ADD) {
-                    uint16_t* d = reinterpret_cast<uint16_t*>(dst) + k;
-                    *d = (uint16_t)f32_to_bf16(__fadd_rn(v, bf16_to_f32(*d)));
-                } else {
-                    reinterpret_cast<uint16_t*>(dst)[k] = reinterpret_cast<const uint16_t*>(src)[k];
-                }
+                if constexpr (F32) reinterpret_cast<float*>(dst)[k] = reinterpret_cast<const float*>(src)[k];
+                else reinterpret_cast<uint16_t*>(dst)[k] = reinterpret_cast<const uint16_t*>(src)[k];
             }
         }
     }
@@ -473,6 +465,8 @@ static int gg_sizes(int64_t rows_max, int E, int N, int D, int dtype, const char
         return fail(MOE_EINVAL, "%s: dtype %d is neither MOE_BF16 nor MOE_F32", name, dtype);
     if (N % 8 || D % 8 || N > MOE_MAX_GROUPED || D > MOE_MAX_GROUPED)
         return fail(MOE_EUNSUPPORTED, "%s: N=%d and D=%d must be multiples of 8 up to %d", name, N, D, MOE_MAX_GROUPED);
+    if (rows_max > MOE_MAX_ROWS)        // a block, or a ring of stages, behind the last row stays in 31 bits
+        return fail(MOE_EUNSUPPORTED, "%s: rows_max=%lld is more than %d", name, (long long)rows_max, MOE_MAX_ROWS);
     return MOE_OK;
 }
 

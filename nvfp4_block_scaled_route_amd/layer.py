@@ -126,7 +126,7 @@ class Fp8Linear:
     x times weight transposed, the weight [N, K] (bf16, K a multiple of 16) quantized
     by load(), x per call. input_grad and weight_grad are its gradients: the former in
     the same format on the transposed weight (with grads=True; N a multiple of 16),
-    the latter in bf16 on x and d_out themselves (N and K multiples of 8). Holds the
+    the latter in bf16 on x and d_out themselves (N and K multiples of 8 up to 32768). Holds the
     buffers of calls with up to max_tokens rows; streams, captures and the life of
     the buffers are as with MxLinear."""
 
@@ -170,7 +170,7 @@ class Fp8Linear:
             raise ValueError(f"{T} tokens, more than the {self.max_tokens} this projection was made for")
         if K != w_codes.shape[1]:
             raise ValueError(f"rows of {K} values, not {w_codes.shape[1]}")
-        codes, sf = self.a_codes[:T * K].view(T, K), self.a_sf[:(K + 127) // 128 * T].view(-1, T)
+        codes, sf = self.a_codes[:T * K].view(T, K), self.a_sf[:(K + 127) // 128 * T].view((K + 127) // 128, T)
         N.fp8_quant(x, codes, sf, stream)
         N.fp8_gemm(codes, sf, w_codes, w_sf, out, stream)
 

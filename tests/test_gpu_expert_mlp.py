@@ -215,3 +215,14 @@ def test_a_batch_of_padding_alone_and_of_no_tokens():
     assert all((t == 0).all() for t in out)
     s = Step(0, 2, 4, 64, 24, 16)
     s.mlp.forward(s.x, s.routing, s.w13, s.w2, s.out)
+
+
+def test_the_backward_of_no_tokens():
+    s = Step(0, 2, 4, 64, 24, 16)
+    s.forward()
+    for accumulate, want in ((True, 1.0), (False, 0.0)):
+        for t in (s.d_w13, s.d_w2):
+            t.fill_(1.0)
+        s.mlp.forward(s.x, s.routing, s.w13, s.w2, s.out)
+        s.backward(accumulate=accumulate)
+        assert (s.d_w13 == want).all() and (s.d_w2 == want).all()

@@ -78,6 +78,19 @@ def test_refusals():
         lin.load(w[:32])
 
 
+def test_no_tokens():
+    """Empty calls; the weight's gradient of none is zeros, or what was there."""
+    lin = LY.Fp8Linear(torch.zeros((48, 144), dtype=torch.bfloat16, device=DEV), 4, grads=True)
+    x, d = (torch.zeros((0, c), dtype=torch.bfloat16, device=DEV) for c in (144, 48))
+    lin(x, torch.empty_like(d))
+    lin.input_grad(d, torch.empty_like(x))
+    d_w = torch.ones((48, 144), device=DEV)
+    lin.weight_grad(d, x, d_w, accumulate=True)
+    assert (d_w == 1).all()
+    lin.weight_grad(d, x, d_w)
+    assert (d_w == 0).all()
+
+
 def test_captured_with_a_step_of_the_weight():
     """Quantizing the weight, the product and its gradients in one graph: replays follow
     the weight and the tokens."""

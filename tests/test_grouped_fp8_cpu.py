@@ -90,6 +90,19 @@ def test_library_refuses_more_threads_than_a_launch_counts(call, kw):
     assert call(**kw) == N.MOE_EUNSUPPORTED, N.lib().moe_last_error()
 
 
+BIG = 0x7FFFF001     # one more than a side may have
+
+
+@pytest.mark.parametrize("call,kw", [
+    (grouped, dict(R=BIG, Nn=8, D=8)), (dgrad, dict(R=BIG, Nn=8, D=8)), (wgrad, dict(R=BIG, Nn=8, D=8)),
+    (quant, dict(T=BIG, H=16, lds=1 << 31)), (quant, dict(T=1, H=BIG + 15, ld=1 << 31)),
+    (quant_weight, dict(Nn=BIG, K=16, ct=None, st=None)), (quant_weight, dict(Nn=1, K=BIG + 15, ld=1 << 31)),
+    (gemm, dict(T=BIG, Nn=1, K=16, lds=1 << 31)), (gemm, dict(T=1, Nn=BIG, K=16, ldo=1 << 31))])
+def test_library_refuses_sides_whose_last_block_leaves_31_bits(call, kw):
+    assert call(**kw) == N.MOE_EUNSUPPORTED, N.lib().moe_last_error()
+    assert b"more than" in N.lib().moe_last_error()
+
+
 @pytest.mark.parametrize("call,kw", [
     (grouped, dict(R=0, x=0)), (grouped, dict(Nn=0, w=0)), (dgrad, dict(R=0, d=0)), (dgrad, dict(D=0)), (wgrad, dict(Nn=0, dw=0)),
     (wgrad, dict(D=0)), (swiglu, dict(R=0, g=0)), (swiglu, dict(I=0)), (swiglu_bwd, dict(R=0)), (quant, dict(T=0, x=0)),
