@@ -38,6 +38,13 @@ __device__ __forceinline__ u32x4 buffer_desc(const void* base) {
     return u32x4{(uint32_t)p, (uint32_t)(p >> 32) & 0xFFFFu, 0x7FFFFFFFu, 0x00020000u};
 }
 
+// A descriptor in scalar registers, which the copies take it from, whatever the compiler keeps its address in.
+__device__ __forceinline__ u32x4 scalar_desc(const void* base) {
+    const uint64_t p = reinterpret_cast<uint64_t>(base);
+    return buffer_desc(reinterpret_cast<const void*>(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(p >> 32)) << 32) |
+                                                     (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)p)));
+}
+
 // Expert weights are read once per call: non-temporal loads keep them from
 // displacing what is read again (metadata, activations, intermediate, rows) in
 // the L2 and Infinity Cache. Measured on decode_b8: expert step 31.3 -> 29.4 us,

@@ -330,13 +330,13 @@ __device__ __forceinline__ void fp_store(const FgArgs& a, uint8_t* slab, const f
 }
 
 // 4 waves, 2 x 2, each MW x NW tiles of 16 x 16; a stage is NB blocks of K.
-template <int MW, int NW, int NB>
+template <int MW, int NW, int NB, int CU>
 struct FgShape {
     static constexpr int kBM = 32 * MW, kBN = 32 * NW, kRow = 128 * NB;
     static constexpr int kACopies = kBM * kRow / 4096, kWCopies = kBN * kRow / 4096, kAll = kACopies + kWCopies + 1;
     static constexpr int kParts = kBM / 64;             // of 64 tokens' scales
     static constexpr int kW = kBM * kRow, kSf = kW + kBN * kRow, kStage = kSf + NB * 4 * kBM;
-    static constexpr int kFit = 80 * 1024 / kStage, kRing = kFit < 4 ? kFit : 4;
+    static constexpr int kFit = 160 / CU * 1024 / kStage, kRing = kFit < 6 ? kFit : 6;
     static constexpr int kSlab = 16 * (32 * NW + 16), kLds = kRing * kStage > 4 * kSlab ? kRing * kStage : 4 * kSlab;
     static_assert(kRing >= 2 && kRing * kAll < 64 && kBM % 64 == 0 && kParts * NB <= 4 && 128 % (16 * NW) == 0, "ring of stages");
 };
@@ -344,9 +344,9 @@ struct FgShape {
 // The operands of a stage are read from LDS into registers while the products of
 // the stage before run, so its buffer is free a stage early, and one barrier a
 // stage does.
-template <int MW, int NW, int NB>
-__global__ void __launch_bounds__(256, 2) fp8_gemm_kernel(FgArgs a) {
-    using S = FgShape<MW, NW, NB>;
+template <int MW, int NW, int NB, int CU>
+__global__ void __launch_bounds__(256, CU) fp8_gemm_kernel(FgArgs a) {
+    using S = FgShape<MW, NW, NB, CU>;
     __shared__ __align__(16) uint8_t lds[S::kLds];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4, wm = wave >> 1, wn = wave & 1;
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(256, 2) fp8_gemm_kernel(FgArgs a) {
     fp_block_of(a.T, a.N, S::kBM, S::kBN, m0, n0);
 
     const int blocks = (a.K + 127) / 128, stages = (blocks + NB - 1) / NB;
-    const u32x4 ra = buffer_desc(a.a + (int64_t)m0 * a.K), rw = buffer_desc(a.w + n0 * a.w_row_stride);
+    const u32x4 ra = scalar_desc(a.a + (int64_t)m0 * a.K), rw = scalar_desc(a.w + n0 * a.w_row_stride);
     constexpr int kRowsPer = 8 / NB;        // rows that an instruction copies
     const int r0 = kRowsPer * wave + lane / (8 * NB), chunk = fp_swizzle<NB>(lane % (8 * NB), r0);      // rows 4 kRowsPer apart have the same
     const uint32_t offa = (uint32_t)(r0 * a.K + chunk * 16), offw = (uint32_t)(r0 * a.w_row_stride + chunk * 16);
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(256, 2) fp8_gemm_kernel(FgArgs a) {
             lds_copy16(rw, __builtin_amdgcn_readfirstlane(at + S::kW + (4 * q + wave) * 1024),
                        in_k && 4 * kRowsPer * q < rows_w ? offw + (uint32_t)(4 * kRowsPer * q * a.w_row_stride) : 0x80000000u, s * S::kRow);
         const int b = s * NB + sblock;      // the tokens' scales; waves may repeat each other's
-        fp_copy4(buffer_desc(a.a_sf + m0 + (b < blocks ? b : 0) * a.a_sf_stride), __builtin_amdgcn_readfirstlane(at + S::kSf + piece * 256),
+        fp_copy4(scalar_desc(a.a_sf + m0 + (b < blocks ? b : 0) * a.a_sf_stride), __builtin_amdgcn_readfirstlane(at + S::kSf + piece * 256),
                  b < blocks ? offs : 0x80000000u, 0u);
     };
     struct Operands {
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_wide_kernel(FgArgs a) {
     fp_block_of(a.T, a.N, S::kSide, S::kSide, m0, n0);
 
     const int stages = (a.K + 127) / 128;
-    const u32x4 ra = buffer_desc(a.a + (int64_t)m0 * a.K), rw = buffer_desc(a.w + n0 * a.w_row_stride);
+    const u32x4 ra = scalar_desc(a.a + (int64_t)m0 * a.K), rw = scalar_desc(a.w + n0 * a.w_row_stride);
     const int r0 = 8 * wn + lane / 8, chunk = fp_swizzle<1>(lane % 8, r0);          // rows 32 apart have the same
     const uint32_t lds0 = lds_addr(lds);
     const uint32_t offa = (uint32_t)(r0 * a.K + chunk * 16), offw = (uint32_t)(r0 * a.w_row_stride + chunk * 16);
@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_wide_kernel(FgArgs a) {
         copy_a(s, 4);
         copy_a(s, 5);
         const int tok = wn * 64 + lane;
-        fp_copy4(buffer_desc(a.a_sf + m0 + (s < stages ? s : 0) * a.a_sf_stride),
+        fp_copy4(scalar_desc(a.a_sf + m0 + (s < stages ? s : 0) * a.a_sf_stride),
                  __builtin_amdgcn_readfirstlane(lds0 + S::kSf + (s & 3) * 1024 + wn * 256),
                  s < stages && m0 + tok < a.T ? (uint32_t)(4 * tok) : 0x80000000u, 0u);
     };
@@ -605,12 +605,12 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_wide_kernel(FgArgs a) {
     }
 }
 
-template <int MW, int NW, int NB>
+template <int MW, int NW, int NB, int CU>
 int launch_fp8(const FgArgs& a, hipStream_t s) {
-    using S = FgShape<MW, NW, NB>;
+    using S = FgShape<MW, NW, NB, CU>;
     const int64_t tiles = (int64_t)((a.T + S::kBM - 1) / S::kBM) * ((a.N + S::kBN - 1) / S::kBN);
     if (!launch_fits(tiles, 256)) return fail(MOE_EUNSUPPORTED, "fp8_gemm: too many output tiles");
-    hipLaunchKernelGGL((fp8_gemm_kernel<MW, NW, NB>), dim3((unsigned)tiles), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((fp8_gemm_kernel<MW, NW, NB, CU>), dim3((unsigned)tiles), dim3(256), 0, s, a);
     return check_launch("fp8_gemm");
 }
 
@@ -701,7 +701,7 @@ extern "C" int fp8_gemm(const uint8_t* a_codes, const float* a_sf, int64_t a_sf_
     if (T <= 16 && N <= 8192) return launch_fp8_skinny<1>(a, s);
     if (T <= 32 && N <= 4096) return launch_fp8_skinny<2>(a, s);
     const auto tiles = [&](int64_t side) { return (T + side - 1) / side * ((N + side - 1) / side); };
-    if (tiles(64) <= 768) return launch_fp8<2, 2, 2>(a, s);
-    if (tiles(128) <= 512) return launch_fp8<4, 4, 1>(a, s);
+    if (tiles(64) <= 768) return launch_fp8<2, 2, 2, 2>(a, s);
+    if (tiles(128) <= 512) return launch_fp8<4, 4, 1, 2>(a, s);
     return launch_fp8_wide(a, s);
 }

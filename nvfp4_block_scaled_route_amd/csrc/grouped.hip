@@ -29,7 +29,7 @@ struct GgArgs {
     const int32_t* counts;
     int E;
     int64_t R;
-    int row_blocks;         // blocks of rows there are at most
+    int blocks;             // of the output there are at most
     int M, N, K;            // output rows (weight gradient), output columns, contraction (else: the expert's rows)
     uint8_t* out;
     int64_t out_stride, out_group;          // bytes
@@ -38,13 +38,6 @@ struct GgArgs {
 
 constexpr int kGgElems = 64;        // contraction of a stage: 128 bytes of a row, a whole cache line
 constexpr uint32_t kOutside = 0x80000000u;      // an offset past the descriptors' range: zeros arrive
-
-// A descriptor in scalar registers, which the copies take it from, whatever the compiler keeps its address in.
-__device__ __forceinline__ u32x4 gg_desc(const uint8_t* base) {
-    const uint64_t p = reinterpret_cast<uint64_t>(base);
-    return buffer_desc(reinterpret_cast<const void*>(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(p >> 32)) << 32) |
-                                                     (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)p)));
-}
 
 // An operand whose rows hold the contraction: ROWS rows x 64 elements in LDS,
 // the 8 chunks of a row permuted so that 16 consecutive rows' reads of one chunk
@@ -65,7 +58,7 @@ struct Along {
         for (int q = 0; q < kCopies; ++q) off[q] = r0 + 32 * q < rows ? (uint32_t)((r0 + 32 * q) * stride + chunk * 16) : kOutside;
     }
     __device__ __forceinline__ void issue(uint32_t lds, int s, int q, int wave) const {
-        lds_copy16(gg_desc(base), __builtin_amdgcn_readfirstlane(lds + (4 * q + wave) * 1024),
+        lds_copy16(scalar_desc(base), __builtin_amdgcn_readfirstlane(lds + (4 * q + wave) * 1024),
                    s * 128 + chunk * 16 < k_bytes ? off[q] : kOutside, (uint32_t)__builtin_amdgcn_readfirstlane(s * 128));
     }
     // 8 elements of the contraction of row `row`: group g's of a step
@@ -81,25 +74,29 @@ struct Along {
 // 64-byte pieces are permuted so that 4 consecutive rows' lie in different banks.
 template <int COLS>
 struct Across {
-    static constexpr int kBytes = 2 * COLS, kChunks = kBytes / 16, kRowsPer = 64 / kChunks;
+    static constexpr int kBytes = 2 * COLS, kChunks = kBytes / 16;
     static constexpr int kCopies = kGgElems * kBytes / 4096, kSize = kGgElems * kBytes;
+    static constexpr bool kWhole = 256 % kChunks == 0;      // whole rows a copy of the 4 waves
     const uint8_t* base;
     int64_t stage;          // bytes from stage to stage
     uint32_t off[kCopies];
-    int row, k;
-    __device__ __forceinline__ static int swizzle(int row) { return COLS >= 128 ? row & 3 : COLS == 64 ? (row >> 1) & 1 : 0; }
+    int row[kWhole ? 1 : kCopies], k;
+    __device__ __forceinline__ static int swizzle(int row) { return COLS % 128 == 0 ? row & 3 : COLS % 64 == 0 ? (row >> 1) & 1 : 0; }
+    __device__ __forceinline__ int row_of(int q) const { return kWhole ? row[0] + 256 / kChunks * q : row[kWhole ? 0 : q]; }
     __device__ __forceinline__ void init(const uint8_t* b, int64_t stride, int cols, int contraction, int wave, int lane) {
         base = b;
         stage = kGgElems * stride;
         k = contraction;
-        row = kRowsPer * wave + lane / kChunks;
-        const int chunk = lane % kChunks ^ (swizzle(row) << 2);     // rows 4 kRowsPer apart have the same
 #pragma unroll
-        for (int q = 0; q < kCopies; ++q) off[q] = chunk * 8 < cols ? (uint32_t)((row + 4 * kRowsPer * q) * stride + chunk * 16) : kOutside;
+        for (int q = 0; q < kCopies; ++q) {
+            const int i = 64 * (4 * q + wave) + lane, r = i / kChunks, chunk = i % kChunks ^ (swizzle(r) << 2);
+            if (!kWhole || q == 0) row[kWhole ? 0 : q] = r;
+            off[q] = chunk * 8 < cols ? (uint32_t)(r * stride + chunk * 16) : kOutside;
+        }
     }
     __device__ __forceinline__ void issue(uint32_t lds, int s, int q, int wave) const {
-        lds_copy16(gg_desc(base + s * stage), __builtin_amdgcn_readfirstlane(lds + (4 * q + wave) * 1024),
-                   s * kGgElems + row + 4 * kRowsPer * q < k ? off[q] : kOutside, 0u);
+        lds_copy16(scalar_desc(base + s * stage), __builtin_amdgcn_readfirstlane(lds + (4 * q + wave) * 1024),
+                   s * kGgElems + row_of(q) < k ? off[q] : kOutside, 0u);
     }
     __device__ __forceinline__ static bf16x8 read(const uint8_t* at, int tile, int step, int lane) {
         typedef __attribute__((address_space(3))) short4v lds4;
@@ -120,6 +117,8 @@ __device__ __forceinline__ int gg_clamp(int v, int low, int high) { return v < l
 struct GgBlock {
     int e, row, rows, end;  // expert, its first row, its rows, the end of its padding rows
     int tile, tiles;        // the block among the expert's, the expert's blocks of rows
+    int side, nt;           // the rows of each but the last, the expert's blocks of columns
+    int tall;               // which of two shapes
 };
 
 __device__ __forceinline__ void gg_rows(const GgArgs& a, int e, GgBlock& b) {
@@ -137,20 +136,48 @@ __device__ __forceinline__ int xcd_run(int total) {
     return j < per + (x < more ? 1 : 0) ? x * per + (x < more ? x : more) + j : -1;
 }
 
-// The expert and block of this workgroup: experts in order, each with
-// ceil(its rows / bm) x nt blocks, padding rows among them. Every thread counts a
-// few experts' blocks; at most `most` blocks of rows in all (more only where the
+// The blocks of rows of an expert: of equal sides, as workgroups that go through
+// the same weights at the same pace share them in the L2 (a small one runs ahead,
+// out of its reach: 128 x 4096 x 1536, 264 rows each, forward 690 -> 628 us, input
+// gradient 657 -> 577). Padding behind the last of up to half a block is that one's
+// too; where there is more, whole blocks.
+__device__ __forceinline__ int gg_split(GgBlock& g, int bm) {
+    const int held = (g.rows + bm - 1) / bm, all = (g.end - g.row + bm - 1 - bm / 2) / bm;
+    g.tiles = g.end == g.row ? 0 : held > all ? held : all > 1 ? all : 1;
+    g.side = held > 1 && held == g.tiles ? ((g.rows + held - 1) / held + 15) & ~15 : bm;
+    return held;
+}
+
+// Blocks of bm x bn or, where an expert's rows fill fewer blocks of them and all its
+// blocks are less work, tall ones (TALL: 320 x 192, 15 tiles a wave against 16).
+template <int BM, int BN, bool TALL>
+__device__ __forceinline__ void gg_shape(int N, GgBlock& g) {
+    const int held = gg_split(g, BM);
+    g.nt = (N + BN - 1) / BN;
+    g.tall = 0;
+    if constexpr (TALL) {
+        GgBlock t = g;
+        t.nt = (N + 191) / 192;
+        t.tall = 1;
+        if (gg_split(t, 320) < held && 15 * t.tiles * t.nt < 16 * g.tiles * g.nt) g = t;
+    }
+}
+
+// The expert and block of this workgroup: experts in order, each with its blocks.
+// Every thread counts a few experts'; at most a.blocks in all (more only where the
 // maps are wrong).
-__device__ __forceinline__ bool gg_find(const GgArgs& a, int bm, int nt, GgBlock& out) {
-    __shared__ int s_sum[4];
-    __shared__ GgBlock s_out;
+template <int BM, int BN, bool TALL>
+__device__ __forceinline__ bool gg_find(const GgArgs& a, GgBlock& out, uint8_t* lds) {
+    int* s_sum = reinterpret_cast<int*>(lds);
+    GgBlock& s_out = *reinterpret_cast<GgBlock*>(lds + 16);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int per = (a.E + 255) / 256, e0 = tid * per;
     int mine = 0;
     for (int e = e0; e < e0 + per && e < a.E; ++e) {
         GgBlock g;
         gg_rows(a, e, g);
-        mine += (g.end - g.row + bm - 1) / bm;
+        gg_shape<BM, BN, TALL>(a.N, g);
+        mine += g.tiles * g.nt;
     }
     const int upto = wave_inclusive_scan(mine);
     if (lane == 63) s_sum[wave] = upto;
@@ -158,17 +185,16 @@ __device__ __forceinline__ bool gg_find(const GgArgs& a, int bm, int nt, GgBlock
     __syncthreads();
     int before = upto - mine, total = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
     for (int w = 0; w < wave; ++w) before += s_sum[w];
-    total = total < a.row_blocks ? total : a.row_blocks;
-    const int id = xcd_run(total * nt), block = id / nt;
+    const int id = xcd_run(total < a.blocks ? total : a.blocks);
     if (id < 0) return false;
-    if (block >= before && block < before + mine) {
+    if (id >= before && id < before + mine) {
         for (int e = e0; e < e0 + per && e < a.E; ++e) {
             GgBlock g;
             gg_rows(a, e, g);
-            g.tiles = (g.end - g.row + bm - 1) / bm;
-            g.tile = id - before * nt;
-            if (block >= before && block < before + g.tiles) s_out = g;
-            before += g.tiles;
+            gg_shape<BM, BN, TALL>(a.N, g);
+            g.tile = id - before;
+            if (id >= before && id < before + g.tiles * g.nt) s_out = g;
+            before += g.tiles * g.nt;
         }
     }
     __syncthreads();
@@ -178,6 +204,10 @@ __device__ __forceinline__ bool gg_find(const GgArgs& a, int bm, int nt, GgBlock
     out.end = __builtin_amdgcn_readfirstlane(s_out.end);
     out.tile = __builtin_amdgcn_readfirstlane(s_out.tile);
     out.tiles = __builtin_amdgcn_readfirstlane(s_out.tiles);
+    out.side = __builtin_amdgcn_readfirstlane(s_out.side);
+    out.nt = __builtin_amdgcn_readfirstlane(s_out.nt);
+    out.tall = __builtin_amdgcn_readfirstlane(s_out.tall);
+    __syncthreads();        // the block's operands come there
     return out.e >= 0;
 }
 
@@ -194,7 +224,8 @@ __device__ __forceinline__ void gg_store(uint8_t* out, int64_t stride, bool vec,
                                          int live, int left, int cols, int lane) {
     constexpr bool kWide = F32 || ADD;      // fp32 in LDS
     constexpr int kRow = gg_row_bytes<NT, kWide>(), kEs = F32 ? 4 : 2, kPiece = 16 / kEs, kPieces = 32 * NT / kPiece;
-    constexpr int kRowsPer = 64 / kPieces, kCount = 32 / kRowsPer;
+    constexpr int kCount = kPieces / 2, kBatch = kCount < 8 ? kCount : kCount / 2;
+    static_assert(kCount % kBatch == 0, "whole batches");
     const int r = lane & 31, g = lane >> 5;
     const bool zero = r >= live;
     wave_lds_sync();
@@ -210,9 +241,11 @@ __device__ __forceinline__ void gg_store(uint8_t* out, int64_t stride, bool vec,
             else *reinterpret_cast<uint2*>(slab + r * kRow + c * 2) = make_uint2(bf16x2_pack(v0, v1), bf16x2_pack(v2, v3));
         }
     wave_lds_sync();
-    const int row = lane / kPieces, c = lane % kPieces * kPiece;
-    const uint8_t* src = slab + row * kRow + c * (kWide ? 4 : 2);
-    uint8_t* dst = out + row * stride + c * kEs;
+    // piece lane + 64 j of the rows' in order
+    const auto row = [&](int j) { return (lane + 64 * j) / kPieces; };
+    const auto col = [&](int j) { return (lane + 64 * j) % kPieces * kPiece; };
+    const auto src = [&](int j) { return slab + row(j) * kRow + col(j) * (kWide ? 4 : 2); };
+    const auto dst = [&](int j) { return out + row(j) * stride + col(j) * kEs; };
     // a piece of the output: what LDS holds, or that and the output's own
     const auto piece = [](const uint8_t* p, u32x4 old) {
         if constexpr (!ADD) {
@@ -232,31 +265,31 @@ __device__ __forceinline__ void gg_store(uint8_t* out, int64_t stride, bool vec,
         }
     };
     if (vec && left >= 32 && cols >= 32 * NT) {
-        constexpr int kBatch = kCount < 8 ? kCount : 8;
 #pragma unroll
         for (int j0 = 0; j0 < kCount; j0 += kBatch) {
             u32x4 v[kBatch] = {};
             if constexpr (ADD) {
 #pragma unroll
-                for (int j = 0; j < kBatch; ++j) v[j] = *reinterpret_cast<const u32x4*>(dst + (j0 + j) * kRowsPer * stride);
+                for (int j = 0; j < kBatch; ++j) v[j] = *reinterpret_cast<const u32x4*>(dst(j0 + j));
             }
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) v[j] = piece(src + (j0 + j) * kRowsPer * kRow, v[j]);
+            for (int j = 0; j < kBatch; ++j) v[j] = piece(src(j0 + j), v[j]);
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) __builtin_nontemporal_store(v[j], reinterpret_cast<u32x4*>(dst + (j0 + j) * kRowsPer * stride));
+            for (int j = 0; j < kBatch; ++j) __builtin_nontemporal_store(v[j], reinterpret_cast<u32x4*>(dst(j0 + j)));
         }
         return;
     }
-    for (int j = 0; j < kCount; ++j, src += kRowsPer * kRow, dst += kRowsPer * stride) {
-        if (row + j * kRowsPer >= left || c >= cols) continue;
+    for (int j = 0; j < kCount; ++j) {
+        const int c = col(j);
+        if (row(j) >= left || c >= cols) continue;
         if (vec && c + kPiece <= cols) {
             u32x4 old = {};
-            if constexpr (ADD) old = *reinterpret_cast<const u32x4*>(dst);
-            *reinterpret_cast<u32x4*>(dst) = piece(src, old);
+            if constexpr (ADD) old = *reinterpret_cast<const u32x4*>(dst(j));
+            *reinterpret_cast<u32x4*>(dst(j)) = piece(src(j), old);
         } else if constexpr (!ADD) {        // rows at any stride; d_w's are contiguous, whole pieces
             for (int k = 0; k < kPiece && c + k < cols; ++k) {
-                if constexpr (F32) reinterpret_cast<float*>(dst)[k] = reinterpret_cast<const float*>(src)[k];
-                else reinterpret_cast<uint16_t*>(dst)[k] = reinterpret_cast<const uint16_t*>(src)[k];
+                if constexpr (F32) reinterpret_cast<float*>(dst(j))[k] = reinterpret_cast<const float*>(src(j))[k];
+                else reinterpret_cast<uint16_t*>(dst(j))[k] = reinterpret_cast<const uint16_t*>(src(j))[k];
             }
         }
     }
@@ -273,52 +306,38 @@ struct GgShape {
     static constexpr int kWN = 4 / WM, kBM = 32 * WM * MW, kBN = 32 * kWN * NW;
     using A = std::conditional_t<KIND == kGgWeight, Across<kBM>, Along<kBM>>;
     using B = std::conditional_t<KIND == kGgRows, Along<kBN>, Across<kBN>>;
-    static constexpr int kAll = A::kCopies + B::kCopies, kStage = A::kSize + B::kSize;
     static constexpr int kSlab = 32 * gg_row_bytes<NW, F32 || ADD>();
-    static constexpr int kPerCu = MW * NW >= 16 || 4 * kStage > 160 * 1024 - 512 ? 1 : 2;
-    static constexpr int kFit = (160 * 1024 / kPerCu - 256) / kStage, kRing = kFit < 6 ? kFit : 6;
-    static constexpr int kLds = kRing * kStage > 4 * kSlab ? kRing * kStage : 4 * kSlab;
-    static_assert(kRing >= 2 && kRing * kAll < 64, "ring of stages");
+    static constexpr bool kTall = KIND != kGgWeight && MW * NW == 16;     // beside tall blocks
+    static constexpr int kPerCu = MW * NW >= 12 ? 1 : 2, kLds = 160 * 1024 / kPerCu;
+    // A ring of stages for a block of LIVE row tiles a wave: what such a block does not need makes room for more of them.
+    template <int LIVE>
+    struct Ring {
+        static constexpr int kCopiesA = KIND == kGgWeight ? A::kCopies : WM * LIVE, kAll = kCopiesA + B::kCopies;
+        static constexpr int kSizeA = 4096 * kCopiesA, kStage = kSizeA + B::kSize;
+        static constexpr int kFit = kLds / kStage, kRing = kFit < 6 ? kFit : 6;
+        static_assert(kRing >= 2 && kRing * kAll < 64, "ring of stages");
+    };
+    static_assert(4 * kSlab <= kLds, "the waves' slabs");
 };
 
-template <int KIND, int WM, int MW, int NW, bool F32, bool ADD>
-__global__ void __launch_bounds__(256, (GgShape<KIND, WM, MW, NW, F32, ADD>::kPerCu)) grouped_gemm_kernel(GgArgs a) {
+// LEAST: no block has fewer row tiles a wave than that (it may have fewer that hold rows).
+template <int KIND, int WM, int MW, int NW, bool F32, bool ADD, int LEAST>
+__device__ __forceinline__ void gg_block(const GgArgs& a, const GgBlock& b, uint8_t* lds) {
     using S = GgShape<KIND, WM, MW, NW, F32, ADD>;
-    constexpr int kAll = S::kAll;
-    __shared__ __align__(16) uint8_t lds[S::kLds];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave / S::kWN, wn = wave % S::kWN;
-
-    GgBlock b;
-    const int nt = (a.N + S::kBN - 1) / S::kBN;
-    if constexpr (KIND == kGgWeight) {
-        b.tiles = (a.M + S::kBM - 1) / S::kBM;
-        const int id = xcd_run(a.E * b.tiles * nt), e = id / (b.tiles * nt);
-        if (id < 0) return;
-        gg_rows(a, e, b);
-        b.tile = id - e * (b.tiles * nt);
-    } else {
-        if (!gg_find(a, S::kBM, nt, b)) return;
-    }
+    const int wm = wave / S::kWN, wn = wave % S::kWN, nt = b.nt;
     // groups of 4 blocks of rows, column by column: what neighbours share stays in the XCD's L2
     const int gm0 = b.tile / (4 * nt) * 4, gh = b.tiles - gm0 < 4 ? b.tiles - gm0 : 4, in = b.tile - gm0 * nt;
-    const int m0 = (gm0 + in % gh) * S::kBM, n0 = (in / gh) * S::kBN;
-    // rows of the block that are computed, and that are written; contraction
-    const int live = KIND == kGgWeight ? a.M - m0 : b.rows - m0, left = KIND == kGgWeight ? live : b.end - b.row - m0;
+    const int mt = gm0 + in % gh, m0 = mt * b.side, n0 = (in / gh) * S::kBN;
+    // rows of the block that are computed, and that are written (the last block has all that are left); contraction
+    const int left = KIND == kGgWeight ? a.M - m0 : mt + 1 < b.tiles ? b.side : b.end - b.row - m0;
+    const int live = KIND == kGgWeight ? left : b.rows - m0 < left ? b.rows - m0 : left;
     const int k = KIND == kGgWeight ? b.rows : live > 0 ? a.K : 0, stages = (k + kGgElems - 1) / kGgElems;
     if (ADD && k == 0) return;
 
     typename S::A ca;
     typename S::B cb;
     const uint32_t lds0 = lds_addr(lds);
-    auto copy = [&](int s, int q0, int q1) __attribute__((always_inline)) {        // copies [q0, q1) of stage s
-        const uint32_t at = lds0 + (s % S::kRing) * S::kStage;
-#pragma unroll
-        for (int q = q0; q < q1; ++q) {
-            if (q < S::A::kCopies) ca.issue(at, s, q, wave);
-            else cb.issue(at + S::A::kSize, s, q - S::A::kCopies, wave);
-        }
-    };
     if (stages > 0) {
         if constexpr (KIND == kGgWeight) {
             ca.init(a.a + b.row * a.a_stride + 2 * (int64_t)m0, a.a_stride, live, k, wave, lane);
@@ -329,8 +348,6 @@ __global__ void __launch_bounds__(256, (GgShape<KIND, WM, MW, NW, F32, ADD>::kPe
             if constexpr (KIND == kGgRows) cb.init(w + n0 * a.b_stride, a.b_stride, a.N - n0, k, wave, lane);
             else cb.init(w + 2 * (int64_t)n0, a.b_stride, a.N - n0, k, wave, lane);
         }
-#pragma unroll
-        for (int s = 0; s < S::kRing; ++s) copy(s, 0, kAll);
     }
     struct Operands {
         bf16x8 a[MW], b[NW];
@@ -348,6 +365,20 @@ __global__ void __launch_bounds__(256, (GgShape<KIND, WM, MW, NW, F32, ADD>::kPe
     // has half a stage more to arrive than the ring has stages.
     auto compute = [&](auto tiles) __attribute__((always_inline)) {
         constexpr int LIVE = decltype(tiles)::value;
+        using R = typename S::template Ring<LIVE>;
+        constexpr int kAll = R::kAll;
+        auto copy = [&](int s, int q0, int q1) __attribute__((always_inline)) {        // copies [q0, q1) of stage s
+            const uint32_t at = lds0 + (s % R::kRing) * R::kStage;
+#pragma unroll
+            for (int q = q0; q < q1; ++q) {
+                if (q < R::kCopiesA) ca.issue(at, s, q, wave);
+                else cb.issue(at + R::kSizeA, s, q - R::kCopiesA, wave);
+            }
+        };
+        if (stages > 0) {
+#pragma unroll
+            for (int s = 0; s < R::kRing; ++s) copy(s, 0, kAll);
+        }
         gg_f16v acc[LIVE][NW];
 #pragma unroll
         for (int m = 0; m < LIVE; ++m)
@@ -358,8 +389,8 @@ __global__ void __launch_bounds__(256, (GgShape<KIND, WM, MW, NW, F32, ADD>::kPe
         if (stages > 0) {
             Operands o0, o1, o2, o3;
             auto read = [&](int s, int step, Operands& o, int i) __attribute__((always_inline)) {  // operand i: the columns', then the rows'
-                const uint8_t* at = lds + (s % S::kRing) * S::kStage;
-                if (i < NW) o.b[i] = S::B::read(at + S::A::kSize, wn * NW + i, step, lane);
+                const uint8_t* at = lds + (s % R::kRing) * R::kStage;
+                if (i < NW) o.b[i] = S::B::read(at + R::kSizeA, wn * NW + i, step, lane);
                 else if (i < NW + LIVE) o.a[i - NW] = S::A::read(at, wm + WM * (i - NW), step, lane);
             };
             auto mfma = [&](const Operands& o, int i) __attribute__((always_inline)) {             // MFMA i of a step
@@ -367,7 +398,7 @@ __global__ void __launch_bounds__(256, (GgShape<KIND, WM, MW, NW, F32, ADD>::kPe
                     acc[i / NW][i % NW] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(o.b[i % NW], o.a[i / NW], acc[i / NW][i % NW], 0, 0, 0);
                 __builtin_amdgcn_sched_barrier(0);
             };
-            __builtin_amdgcn_s_waitcnt(vmcnt_at_most((S::kRing - 1) * kAll));
+            __builtin_amdgcn_s_waitcnt(vmcnt_at_most((R::kRing - 1) * kAll));
             asm volatile("s_barrier" ::: "memory");
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -387,10 +418,10 @@ __global__ void __launch_bounds__(256, (GgShape<KIND, WM, MW, NW, F32, ADD>::kPe
                         asm volatile("s_barrier" ::: "memory");
                         __builtin_amdgcn_sched_barrier(0);
                     }
-                    if (i >= kFree) copy(s + S::kRing, (i - kFree) * kAll / kCopySlots, (i - kFree + 1) * kAll / kCopySlots);
+                    if (i >= kFree) copy(s + R::kRing, (i - kFree) * kAll / kCopySlots, (i - kFree + 1) * kAll / kCopySlots);
                     mfma(i < kSlots ? o1 : o2, i % kSlots);
                 }
-                __builtin_amdgcn_s_waitcnt(vmcnt_at_most((S::kRing - 1) * kAll));
+                __builtin_amdgcn_s_waitcnt(vmcnt_at_most((R::kRing - 1) * kAll));
                 asm volatile("s_barrier" ::: "memory");
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -417,22 +448,51 @@ __global__ void __launch_bounds__(256, (GgShape<KIND, WM, MW, NW, F32, ADD>::kPe
                                    a.N - c0, lane);
             __builtin_amdgcn_sched_barrier(0);
         }
-        // rows of padding behind those tiles
+        // rows of padding behind those tiles: whole pieces of 16 bytes (N % 8 == 0) where rows start at such
         if constexpr (KIND != kGgWeight) {
-            for (int r = 32 * WM * LIVE + wm; r < left && r < S::kBM; r += WM) {
-                uint8_t* out = a.out + (b.row + (int64_t)m0 + r) * a.out_stride;
-                for (int n = c0 + lane; n < c0 + 32 * NW && n < a.N; n += 64) {
-                    if constexpr (F32) reinterpret_cast<float*>(out)[n] = 0.0f;
-                    else reinterpret_cast<uint16_t*>(out)[n] = 0;
-                }
+            constexpr int kEs = F32 ? 4 : 2, kPieces = 2 * NW * kEs;
+            for (int i = lane; i < (left - 32 * WM * LIVE) * kPieces; i += 64) {
+                const int r = 32 * WM * LIVE + i / kPieces, c = c0 * kEs + i % kPieces * 16;
+                if (r % WM != wm || c >= a.N * kEs) continue;
+                uint8_t* out = a.out + (b.row + (int64_t)m0 + r) * a.out_stride + c;
+                if (a.out_vec) __builtin_nontemporal_store(u32x4{}, reinterpret_cast<u32x4*>(out));
+                else
+                    for (int k = 0; k < 16 / kEs; ++k) {
+                        if constexpr (F32) reinterpret_cast<float*>(out)[k] = 0.0f;
+                        else reinterpret_cast<uint16_t*>(out)[k] = 0;
+                    }
             }
         }
     };
     const int tiles = (live + 32 * WM - 1) / (32 * WM);
-    if (MW >= 4 && tiles >= 4) compute(std::integral_constant<int, (MW >= 4 ? 4 : 1)>());
-    else if (MW >= 3 && tiles >= 3) compute(std::integral_constant<int, (MW >= 3 ? 3 : 1)>());
-    else if (MW >= 2 && tiles >= 2) compute(std::integral_constant<int, (MW >= 2 ? 2 : 1)>());
-    else compute(std::integral_constant<int, 1>());
+    if (MW >= 5 && (LEAST >= 5 || tiles >= 5)) compute(std::integral_constant<int, (MW >= 5 ? 5 : 1)>());
+    else if constexpr (LEAST < 5) {
+        if (MW >= 4 && tiles >= 4) compute(std::integral_constant<int, (MW >= 4 ? 4 : 1)>());
+        else if (MW >= 3 && tiles >= 3) compute(std::integral_constant<int, (MW >= 3 ? 3 : 1)>());
+        else if (MW >= 2 && tiles >= 2) compute(std::integral_constant<int, (MW >= 2 ? 2 : 1)>());
+        else compute(std::integral_constant<int, 1>());
+    }
+}
+
+template <int KIND, int WM, int MW, int NW, bool F32, bool ADD>
+__global__ void __launch_bounds__(256, (GgShape<KIND, WM, MW, NW, F32, ADD>::kPerCu)) grouped_gemm_kernel(GgArgs a) {
+    using S = GgShape<KIND, WM, MW, NW, F32, ADD>;
+    __shared__ __align__(16) uint8_t lds[S::kLds];
+    GgBlock b;
+    if constexpr (KIND == kGgWeight) {
+        b.tiles = (a.M + S::kBM - 1) / S::kBM;
+        b.nt = (a.N + S::kBN - 1) / S::kBN;
+        b.side = S::kBM;
+        const int id = xcd_run(a.blocks), e = id / (b.tiles * b.nt);
+        if (id < 0) return;
+        gg_rows(a, e, b);
+        b.tile = id - e * (b.tiles * b.nt);
+    } else {
+        if (!gg_find<S::kBM, S::kBN, S::kTall>(a, b, lds)) return;
+        if constexpr (S::kTall)
+            if (b.tall) return gg_block<KIND, 2, 5, 3, F32, ADD, 5>(a, b, lds);
+    }
+    gg_block<KIND, WM, MW, NW, F32, ADD, 1>(a, b, lds);
 }
 
 // ------------------------------------------------------------------ host side
@@ -441,10 +501,11 @@ int launch_grouped(GgArgs a, hipStream_t s, const char* name) {
     using S = GgShape<KIND, WM, MW, NW, F32, ADD>;
     const int64_t nt = (a.N + S::kBN - 1) / S::kBN;
     const int64_t row_blocks = a.R / S::kBM + (a.R < a.E ? a.R : a.E);      // whole blocks, and each expert's last
-    const int64_t blocks = KIND == kGgWeight ? (int64_t)a.E * ((a.M + S::kBM - 1) / S::kBM) * nt : row_blocks * nt;
+    int64_t blocks = KIND == kGgWeight ? (int64_t)a.E * ((a.M + S::kBM - 1) / S::kBM) * nt : row_blocks * nt;
+    if (S::kTall) blocks += blocks / 15;        // tall ones where they are fewer, or up to so many more
     const int64_t grid = (blocks + 7) / 8 * 8;
     if (!launch_fits(grid, 256)) return fail(MOE_EUNSUPPORTED, "%s: too many output tiles", name);
-    a.row_blocks = (int)row_blocks;
+    a.blocks = (int)blocks;
     hipLaunchKernelGGL((grouped_gemm_kernel<KIND, WM, MW, NW, F32, ADD>), dim3((unsigned)grid), dim3(256), 0, s, a);
     return check_launch(name);
 }

@@ -133,6 +133,19 @@ def test_blocks_of_256_rows(deep, grad, dt):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("counts,align,gap,out_pad", [
+    ([257, 288, 300, 320, 321, 513, 640, 641], 1, 0, 0), ([769, 961, 1100, 640, 257, 1], 128, 0, 3),
+    ([300, 257, 620, 0, 255, 1500], 16, 400, 0), ([4500], 128, 0, 8)])
+def test_blocks_of_320_rows(counts, align, gap, out_pad, grad, dt):
+    """Experts whose rows fill fewer blocks of 320 x 192 than of 256 x 256, beside others:
+    equal sides, a last block of padding alone, rows that start anywhere."""
+    r = Rows(counts, align, gap, seed=len(counts))
+    wide, deep = 6400, 136
+    _rows_call(r, *((deep, wide) if grad else (wide, deep)), dt, grad, out_pad=out_pad)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("accumulate", [False, True])
 def test_weight_grad_blocks_of_256(accumulate, dt):
     r = Rows([0, 1, 63, 64, 65, 400, 700, 300], 16, 0, seed=3)
