@@ -315,40 +315,52 @@ __device__ __forceinline__ void fp_store(const FgArgs& a, uint8_t* slab, const f
         *reinterpret_cast<uint2*>(slab + r * kOutRow + 2 * (16 * n + 4 * g)) =
             make_uint2(bf16x2_pack(acc[n][0], acc[n][1]), bf16x2_pack(acc[n][2], acc[n][3]));
     wave_lds_sync();
+    if (a.out_vec && a.N % 8 == 0) {
 #pragma unroll
-    for (int j = 0; j < (NW + 1) / 2; ++j) {        // 2 NW pieces of 16 bytes a row
-        const int i = lane + 64 * j, row = i / (2 * NW), c = i % (2 * NW) * 8;
-        if (row >= 16 || t0 + row >= a.T || c0 + c >= a.N) continue;
-        uint16_t* dst = a.out + (t0 + row) * a.out_stride + c0 + c;
-        const uint16_t* src = reinterpret_cast<const uint16_t*>(slab + row * kOutRow + 2 * c);
-        if (a.out_vec && c0 + c + 8 <= a.N) {
-            __builtin_nontemporal_store(*reinterpret_cast<const u32x4*>(src), reinterpret_cast<u32x4*>(dst));
-        } else {
-            for (int k = 0; k < 8 && c0 + c + k < a.N; ++k) dst[k] = src[k];
+        for (int j = 0; j < (NW + 1) / 2; ++j) {        // 2 NW pieces of 16 bytes a row
+            const int i = lane + 64 * j, row = i / (2 * NW), c = i % (2 * NW) * 8;
+            if (row >= 16 || t0 + row >= a.T || c0 + c >= a.N) continue;
+            __builtin_nontemporal_store(*reinterpret_cast<const u32x4*>(slab + row * kOutRow + 2 * c),
+                                        reinterpret_cast<u32x4*>(a.out + (t0 + row) * a.out_stride + c0 + c));
         }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4 * NW; ++j) {                  // a row's values by consecutive lanes
+        const int i = lane + 64 * j, row = i / (16 * NW), c = i % (16 * NW);
+        if (t0 + row < a.T && c0 + c < a.N)
+            a.out[(t0 + row) * a.out_stride + c0 + c] = *reinterpret_cast<const uint16_t*>(slab + row * kOutRow + 2 * c);
     }
 }
 
-// 4 waves, 2 x 2, each MW x NW tiles of 16 x 16; a stage is NB blocks of K.
-template <int MW, int NW, int NB, int CU>
+// 4 waves, 2 x 2, each MW x NW tiles of 16 x 16; a stage is NB blocks of K. KS such
+// groups of waves with a ring each take turns at the stages.
+template <int MW, int NW, int NB, int KS>
 struct FgShape {
     static constexpr int kBM = 32 * MW, kBN = 32 * NW, kRow = 128 * NB;
     static constexpr int kACopies = kBM * kRow / 4096, kWCopies = kBN * kRow / 4096, kAll = kACopies + kWCopies + 1;
     static constexpr int kParts = kBM / 64;             // of 64 tokens' scales
     static constexpr int kW = kBM * kRow, kSf = kW + kBN * kRow, kStage = kSf + NB * 4 * kBM;
-    static constexpr int kFit = 160 / CU * 1024 / kStage, kRing = kFit < 6 ? kFit : 6;
-    static constexpr int kSlab = 16 * (32 * NW + 16), kLds = kRing * kStage > 4 * kSlab ? kRing * kStage : 4 * kSlab;
+    static constexpr int kFit = 80 * 1024 / kStage, kRing = kFit < 4 ? kFit : 4;
+    static constexpr int kSlab = 16 * (32 * NW + 16), kGroup = kRing * kStage, kLds = KS * kGroup;
+    static_assert(4 * KS * kSlab <= kGroup && 4096 * MW * NW <= kGroup, "the waves' slabs and sums");
     static_assert(kRing >= 2 && kRing * kAll < 64 && kBM % 64 == 0 && kParts * NB <= 4 && 128 % (16 * NW) == 0, "ring of stages");
 };
 
-// The operands of a stage are read from LDS into registers while the products of
-// the stage before run, so its buffer is free a stage early, and one barrier a
-// stage does.
-template <int MW, int NW, int NB, int CU>
-__global__ void __launch_bounds__(256, CU) fp8_gemm_kernel(FgArgs a) {
-    using S = FgShape<MW, NW, NB, CU>;
-    __shared__ __align__(16) uint8_t lds[S::kLds];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+// The operands of a turn are read from LDS into registers while the products of the
+// turn before run, so its buffer is free a turn early, and one barrier a turn does.
+// A wave alone on its SIMD waits for each instruction it issues: copies, reads and
+// sums are spread between the MFMAs (512 x 4096 x 4096 64 x 128 20.3 -> 15.5 us), and
+// where the blocks are fewer than the CUs a second group of waves takes half of K
+// (256 x 4096 x 4096 13.2 -> 10.9 us). 512 x 4096 x 4096 in 14.9 us: 1.15 PFLOP/s; rows
+// that start inside a cache line cost their copies twice the lines (517 x 2088, K =
+// 4096 14.4 us, K = 4112 18.1).
+template <int MW, int NW, int NB, int KS>
+__global__ void __launch_bounds__(256 * KS, 2) fp8_gemm_kernel(FgArgs a) {
+    using S = FgShape<MW, NW, NB, KS>;
+    __shared__ __align__(16) uint8_t all[S::kLds];
+    const int lane = threadIdx.x & 63, w8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), group = w8 >> 2, wave = w8 & 3;
+    uint8_t* lds = all + group * S::kGroup;
     const int r = lane & 15, g = lane >> 4, wm = wave >> 1, wn = wave & 1;
     int m0, n0;
     fp_block_of(a.T, a.N, S::kBM, S::kBN, m0, n0);
@@ -362,43 +374,45 @@ __global__ void __launch_bounds__(256, CU) fp8_gemm_kernel(FgArgs a) {
     const int piece = wave % (S::kParts * NB), sblock = piece / S::kParts, stok = piece % S::kParts * 64 + lane;
     const uint32_t offs = m0 + stok < a.T ? (uint32_t)(4 * stok) : 0x80000000u;
     const uint32_t lds0 = lds_addr(lds);
-    auto copy = [&](int s) __attribute__((always_inline)) {
-        const uint32_t at = lds0 + (s % S::kRing) * S::kStage;
+    // copy q of the group's turn i (stage KS i + group): tokens', weights', scales'
+    auto copy = [&](int i, int q) __attribute__((always_inline)) {
+        const uint32_t at = lds0 + (i % S::kRing) * S::kStage;
+        const int s = KS * i + group;
         const bool in_k = s * S::kRow + chunk * 16 < a.K;
-#pragma unroll
-        for (int q = 0; q < S::kACopies; ++q)
+        if (q < S::kACopies) {
             lds_copy16(ra, __builtin_amdgcn_readfirstlane(at + (4 * q + wave) * 1024),
                        in_k && 4 * kRowsPer * q < rows_a ? offa + (uint32_t)(4 * kRowsPer * q * a.K) : 0x80000000u, s * S::kRow);
-#pragma unroll
-        for (int q = 0; q < S::kWCopies; ++q)
+        } else if (q < S::kAll - 1) {
+            q -= S::kACopies;
             lds_copy16(rw, __builtin_amdgcn_readfirstlane(at + S::kW + (4 * q + wave) * 1024),
                        in_k && 4 * kRowsPer * q < rows_w ? offw + (uint32_t)(4 * kRowsPer * q * a.w_row_stride) : 0x80000000u, s * S::kRow);
-        const int b = s * NB + sblock;      // the tokens' scales; waves may repeat each other's
-        fp_copy4(scalar_desc(a.a_sf + m0 + (b < blocks ? b : 0) * a.a_sf_stride), __builtin_amdgcn_readfirstlane(at + S::kSf + piece * 256),
-                 b < blocks ? offs : 0x80000000u, 0u);
+        } else {
+            const int b = s * NB + sblock;      // waves may repeat each other's
+            fp_copy4(scalar_desc(a.a_sf + m0 + (b < blocks ? b : 0) * a.a_sf_stride), __builtin_amdgcn_readfirstlane(at + S::kSf + piece * 256),
+                     b < blocks ? offs : 0x80000000u, 0u);
+        }
     };
     struct Operands {
         FpFrag w[NB][NW], a[NB][MW];
         float sa[NB][MW];
     };
-    auto read = [&](int s, Operands& o) __attribute__((always_inline)) {
+    // Read i of a turn's kReads: of each block the weights, then the tokens with their scale.
+    constexpr int kReads = NB * (NW + MW);
+    auto read = [&](int s, Operands& o, int i) __attribute__((always_inline)) {
         const uint8_t* at = lds + (s % S::kRing) * S::kStage;
-        auto frag = [&](const uint8_t* rows, int row, int b) __attribute__((always_inline)) {
+        const int b = i / (NW + MW), j = i % (NW + MW);
+        auto frag = [&](const uint8_t* rows, int row) __attribute__((always_inline)) {
             FpFrag f;
             f.q[0] = *reinterpret_cast<const uint4*>(rows + row * S::kRow + 16 * fp_swizzle<NB>(8 * b + g, row));
             f.q[1] = *reinterpret_cast<const uint4*>(rows + row * S::kRow + 16 * fp_swizzle<NB>(8 * b + 4 + g, row));
             return f;
         };
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-#pragma unroll
-            for (int n = 0; n < NW; ++n) o.w[b][n] = frag(at + S::kW, 16 * (wn * NW + n) + r, b);
-#pragma unroll
-            for (int m = 0; m < MW; ++m) {
-                const int row = 16 * (wm * MW + m) + r;
-                o.a[b][m] = frag(at, row, b);
-                o.sa[b][m] = *reinterpret_cast<const float*>(at + S::kSf + 4 * (b * S::kBM + row));
-            }
+        if (j < NW) {
+            o.w[b][j] = frag(at + S::kW, 16 * (wn * NW + j) + r);
+        } else {
+            const int row = 16 * (wm * MW + j - NW) + r;
+            o.a[b][j - NW] = frag(at, row);
+            o.sa[b][j - NW] = *reinterpret_cast<const float*>(at + S::kSf + 4 * (b * S::kBM + row));
         }
     };
     // this wave's columns lie in one block of w's scales; lane i holds that of block 64 j + i
@@ -413,44 +427,76 @@ __global__ void __launch_bounds__(256, CU) fp8_gemm_kernel(FgArgs a) {
     auto stage = [&](int s, const Operands& o, Operands& next) __attribute__((always_inline)) {
         __builtin_amdgcn_s_waitcnt(vmcnt_at_most((S::kRing - 2) * S::kAll) & lgkmcnt_zero());
         asm volatile("s_barrier" ::: "memory");
-        copy(s + S::kRing);
-        read(s + 1, next);
-        __builtin_amdgcn_sched_barrier(0);
+        // between the products: the copies of turn s + kRing, the reads of turn s + 1, the sums two products ago
+        constexpr int kSlots = NB * MW * NW;
+        floatx4 t[3];
+        float f = 0.0f, last = 0.0f;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            const float sw = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(sw64), (s * NB + b) & 63));
+        for (int i = 0; i < kSlots + 2; ++i) {
+            const int b = i / (MW * NW), m = i / NW % MW, n = i % NW;
+            if (i < kSlots) {
+                if (n == 0) {
+                    last = f;
+                    f = __fmul_rn(o.sa[b][m], __int_as_float(__builtin_amdgcn_readlane(__float_as_int(sw64), ((KS * s + group) * NB + b) & 63)));
+                }
+                t[i % 3] = fp_mfma(o.w[b][n], o.a[b][m]);
 #pragma unroll
-            for (int m = 0; m < MW; ++m) {
-                floatx4 t[NW];
+                for (int q = i * S::kAll / kSlots; q < (i + 1) * S::kAll / kSlots; ++q) copy(s + S::kRing, q);
 #pragma unroll
-                for (int n = 0; n < NW; ++n) t[n] = fp_mfma(o.w[b][n], o.a[b][m]);
-                const float f = __fmul_rn(o.sa[b][m], sw);
-#pragma unroll
-                for (int n = 0; n < NW; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[m][n][i] = __fmaf_rn(f, t[n][i], acc[m][n][i]);
+                for (int q = i * kReads / kSlots; q < (i + 1) * kReads / kSlots; ++q) read(s + 1, next, q);
             }
+            if (i >= 2) {
+                const int p = i - 2;
+                const float scale = i >= kSlots || p / NW == i / NW ? f : last;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[p / NW % MW][p % NW][k] = __fmaf_rn(scale, t[p % 3][k], acc[p / NW % MW][p % NW][k]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
-    static_assert(64 % (2 * NB) == 0, "a pair of stages lies in 64 blocks");
+    static_assert(64 % (2 * KS * NB) == 0, "a pair of turns lies in 64 blocks");
 #pragma unroll
-    for (int s = 0; s < S::kRing; ++s) copy(s);
+    for (int s = 0; s < S::kRing; ++s)
+#pragma unroll
+        for (int q = 0; q < S::kAll; ++q) copy(s, q);
     Operands o0, o1;
     __builtin_amdgcn_s_waitcnt(vmcnt_at_most((S::kRing - 1) * S::kAll));
     __syncthreads();
-    read(0, o0);
-    for (int s = 0; s < stages; s += 2) {
-        if ((s * NB & 63) == 0) sw64 = fp_load_wait(wsf + s * NB + lane, cols && s * NB + lane < blocks);
+#pragma unroll
+    for (int i = 0; i < kReads; ++i) read(0, o0, i);
+    const int turns = (stages + KS - 1) / KS;       // of either group: stages behind the last are zeros
+    for (int s = 0; s < turns; s += 2) {
+        if ((s * KS * NB & 63) == 0) sw64 = fp_load_wait(wsf + s * KS * NB + lane, cols && s * KS * NB + lane < blocks);
         stage(s, o0, o1);
-        if (s + 1 < stages) stage(s + 1, o1, o0);
+        if (s + 1 < turns) stage(s + 1, o1, o0);
     }
-    // the copies of the stages behind the last still write to the LDS
+    // the copies of the turns behind the last still write to the LDS
     __builtin_amdgcn_s_waitcnt(vmcnt_at_most(0) & lgkmcnt_zero());
     __syncthreads();
+    // of two groups' sums each group stores half: the other's comes through LDS
+    constexpr int kMine = MW / KS;
+    if constexpr (KS == 2) {
+        floatx4* sums = reinterpret_cast<floatx4*>(all) + (wave * MW * NW) * 64 + lane;
+        static_assert(MW % 2 == 0, "halves");
+#pragma unroll
+        for (int m = 0; m < MW; ++m)
+            if (m / kMine != group) {
+#pragma unroll
+                for (int n = 0; n < NW; ++n) sums[64 * (m * NW + n)] = acc[m][n];
+            }
+        __syncthreads();
+#pragma unroll
+        for (int m = 0; m < MW; ++m)
+            if (m / kMine == group) {
+#pragma unroll
+                for (int n = 0; n < NW; ++n) acc[m][n] += sums[64 * (m * NW + n)];
+            }
+    }
+    uint8_t* slab = KS == 2 ? all + S::kGroup + (4 * group + wave) * S::kSlab : all + wave * S::kSlab;      // clear of the sums
 #pragma unroll
     for (int m = 0; m < MW; ++m) {
         const int t0 = m0 + 16 * (wm * MW + m);
-        if (t0 < a.T && cols) fp_store<NW>(a, lds + wave * S::kSlab, acc[m], t0, n0 + 16 * NW * wn, lane);
+        if (m / kMine == group && t0 < a.T && cols) fp_store<NW>(a, slab, acc[m], t0, n0 + 16 * NW * wn, lane);
     }
 }
 
@@ -605,12 +651,12 @@ __global__ void __launch_bounds__(512, 2) fp8_gemm_wide_kernel(FgArgs a) {
     }
 }
 
-template <int MW, int NW, int NB, int CU>
+template <int MW, int NW, int NB, int KS>
 int launch_fp8(const FgArgs& a, hipStream_t s) {
-    using S = FgShape<MW, NW, NB, CU>;
+    using S = FgShape<MW, NW, NB, KS>;
     const int64_t tiles = (int64_t)((a.T + S::kBM - 1) / S::kBM) * ((a.N + S::kBN - 1) / S::kBN);
-    if (!launch_fits(tiles, 256)) return fail(MOE_EUNSUPPORTED, "fp8_gemm: too many output tiles");
-    hipLaunchKernelGGL((fp8_gemm_kernel<MW, NW, NB, CU>), dim3((unsigned)tiles), dim3(256), 0, s, a);
+    if (!launch_fits(tiles, 256 * KS)) return fail(MOE_EUNSUPPORTED, "fp8_gemm: too many output tiles");
+    hipLaunchKernelGGL((fp8_gemm_kernel<MW, NW, NB, KS>), dim3((unsigned)tiles), dim3(256 * KS), 0, s, a);
     return check_launch("fp8_gemm");
 }
 
@@ -692,16 +738,20 @@ extern "C" int fp8_gemm(const uint8_t* a_codes, const float* a_sf, int64_t a_sf_
     if (out_row_stride < N) return fail(MOE_EINVAL, "%s: out row stride %lld must be >= N", name, (long long)out_row_stride);
     FgArgs a{a_codes, a_sf, a_sf_stride, w_codes, w_row_stride, w_sf, T, N, K, out, out_row_stride, out_row_stride % 8 == 0 ? 1 : 0};
     hipStream_t s = (hipStream_t)stream;
-    // us, K = 4096, replayed from a graph: by columns, blocks of 64 x 64, 128 x 128, 256 x 256
-    //   1 x 4096   5.1 11.3 27.3 47.0     16 x 8192  10.4 12.3 27.7 48.1      1 x 16384 13.8 13.7 27.7 48.8
-    //  32 x 4096   8.8 11.9 27.7 48.1     32 x 8192  15.3 12.7 28.0 48.3    512 x 4096    -  15.9 29.2 50.5
-    // 768 x 4096    -  26.1 29.8 51.0   1024 x 4096    -  31.1 30.0 50.6   2048 x 4096    -  60.2 42.3 52.4
-    // 4096 x 4096   -   118 81.5 68.5   8192 x 8192    -   435  299  246
-    // (two of the smaller blocks run on a CU: 512 at once)
+    // us, K = 4096, replayed from a graph: by columns, blocks of 64 x 64 with two groups of waves, of 64 x 128 with two
+    // and with one, 128 x 128, 256 x 256
+    //    1 x 4096   5.1 10.1 13.3 15.0 24.3 47     16 x 8192  10.4 10.1 13.0 14.8 24.3 48      1 x 16384 13.8 12.6 13.2 14.8 24.7 49
+    //   32 x 4096   8.4 10.1 13.3 15.0 24.3 48    256 x 4096    -  10.9 13.8 15.4 25.2 49    512 x 4096    -  20.7 14.9 16.7 26.0 50
+    //  768 x 4096    -  29.4 26.3 22.2 26.8 50   1024 x 4096    -  39.4 28.8 25.4 27.6 50   1280 x 4096    -  49.0 40.0 36.1 32.6 50
+    // 2048 x 4096    -  74.9 55.9 49.7 38.8 52   3000 x 4096    -   111 83.8 72.9 60.9 55   8192 x 8192    -   555  421  362  287 245
+    // Few blocks of K do not pay for a second group's sums: 64 x 64 with two groups and with one (stages of two blocks)
+    // 64 x 2048 x 1024 5.0 and 4.5, 33 x 4096 x 2048 6.5 and 6.0, 64 x 8192 x 4096 10.3 and 13.7
     if (T <= 16 && N <= 8192) return launch_fp8_skinny<1>(a, s);
     if (T <= 32 && N <= 4096) return launch_fp8_skinny<2>(a, s);
-    const auto tiles = [&](int64_t side) { return (T + side - 1) / side * ((N + side - 1) / side); };
-    if (tiles(64) <= 768) return launch_fp8<2, 2, 2, 2>(a, s);
-    if (tiles(128) <= 512) return launch_fp8<4, 4, 1, 2>(a, s);
+    const auto tiles = [&](int64_t rows, int64_t cols) { return (T + rows - 1) / rows * ((N + cols - 1) / cols); };
+    if (tiles(64, 64) <= 256) return K > 2048 ? launch_fp8<2, 2, 1, 2>(a, s) : launch_fp8<2, 2, 2, 1>(a, s);
+    if (tiles(64, 128) <= 256) return launch_fp8<2, 4, 1, 2>(a, s);
+    if (tiles(64, 128) <= 512) return launch_fp8<2, 4, 1, 1>(a, s);
+    if (tiles(128, 128) <= 512) return launch_fp8<4, 4, 1, 1>(a, s);
     return launch_fp8_wide(a, s);
 }

@@ -142,6 +142,26 @@ def test_blocks_of_64(T, Nn, K):
     _product(T, Nn, K)
 
 
+@pytest.mark.parametrize("T,Nn,K", [(517, 2085, 4112), (258, 7001, 16), (260, 6000, 8208), (449, 4090, 1040), (600, 4096, 1552),
+                                    (1024, 4095, 272), (513, 7000, 8336)])
+def test_blocks_of_64_by_128(T, Nn, K):
+    """At most 256 of them, by two groups of waves, and at most 512, by one."""
+    _product(T, Nn, K)
+    _product(T, Nn, K, out_pad=1)
+
+
+@pytest.mark.parametrize("T,Nn,K", [(33, 70, 2064), (33, 70, 2176), (70, 130, 4096), (256, 4000, 2304), (40, 16200, 2208)])
+def test_two_groups_of_waves(T, Nn, K):
+    """Odd and even numbers of blocks of K, and the group that gets one less."""
+    _product(T, Nn, K, w_pad=16, out_pad=5)
+    _, t = _operands(np.random.default_rng(T), T, Nn, K)
+    outs = [torch.empty((T, Nn), dtype=torch.bfloat16, device=DEV) for _ in range(3)]
+    for o in outs:
+        N.fp8_gemm(*t, o)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, outs[0]) for o in outs)
+
+
 @pytest.mark.parametrize("T,Nn,K", [(1100, 3000, 144), (2000, 2100, 272), (1025, 4000, 128), (2048, 3999, 16)])
 def test_blocks_of_128(T, Nn, K):
     _product(T, Nn, K)
