@@ -241,11 +241,16 @@ __device__ __forceinline__ void gg_store(uint8_t* out, int64_t stride, bool vec,
             else *reinterpret_cast<uint2*>(slab + r * kRow + c * 2) = make_uint2(bf16x2_pack(v0, v1), bf16x2_pack(v2, v3));
         }
     wave_lds_sync();
-    // piece lane + 64 j of the rows' in order
-    const auto row = [&](int j) { return (lane + 64 * j) / kPieces; };
-    const auto col = [&](int j) { return (lane + 64 * j) % kPieces * kPiece; };
-    const auto src = [&](int j) { return slab + row(j) * kRow + col(j) * (kWide ? 4 : 2); };
-    const auto dst = [&](int j) { return out + row(j) * stride + col(j) * kEs; };
+    // piece lane + 64 j of the rows' in order: where 64 are whole rows, from j to j the same rows further down
+    constexpr bool kEven = 64 % kPieces == 0;
+    constexpr int kRowsPer = kEven ? 64 / kPieces : 0;
+    const int lane_row = lane / kPieces, lane_col = lane % kPieces * kPiece;
+    const auto row = [&](int j) { return kEven ? lane_row + j * kRowsPer : (lane + 64 * j) / kPieces; };
+    const auto col = [&](int j) { return kEven ? lane_col : (lane + 64 * j) % kPieces * kPiece; };
+    const uint8_t* src0 = slab + lane_row * kRow + lane_col * (kWide ? 4 : 2);
+    uint8_t* dst0 = out + lane_row * stride + lane_col * kEs;
+    const auto src = [&](int j) { return kEven ? src0 + j * kRowsPer * kRow : slab + row(j) * kRow + col(j) * (kWide ? 4 : 2); };
+    const auto dst = [&](int j) { return kEven ? dst0 + j * kRowsPer * stride : out + row(j) * stride + col(j) * kEs; };
     // a piece of the output: what LDS holds, or that and the output's own
     const auto piece = [](const uint8_t* p, u32x4 old) {
         if constexpr (!ADD) {
@@ -279,13 +284,14 @@ __device__ __forceinline__ void gg_store(uint8_t* out, int64_t stride, bool vec,
         }
         return;
     }
+#pragma unroll 1
     for (int j = 0; j < kCount; ++j) {
         const int c = col(j);
         if (row(j) >= left || c >= cols) continue;
         if (vec && c + kPiece <= cols) {
             u32x4 old = {};
             if constexpr (ADD) old = *reinterpret_cast<const u32x4*>(dst(j));
-            *reinterpret_cast<u32x4*>(dst(j)) = piece(src(j), old);
+            __builtin_nontemporal_store(piece(src(j), old), reinterpret_cast<u32x4*>(dst(j)));
         } else if constexpr (!ADD) {        // rows at any stride; d_w's are contiguous, whole pieces
             for (int k = 0; k < kPiece && c + k < cols; ++k) {
                 if constexpr (F32) reinterpret_cast<float*>(dst(j))[k] = reinterpret_cast<const float*>(src(j))[k];
@@ -299,6 +305,14 @@ __device__ __forceinline__ void gg_store(uint8_t* out, int64_t stride, bool vec,
 // 4 waves, WM along the output's rows; a wave has MW x NW tiles of 32 x 32, its
 // tiles' rows dealt round the waves, so that a block of few rows is few tiles of
 // every wave's.
+//
+// What bounds it: 128 experts x 4096 x 1536, 4096 tokens top-8, in 492 us forward is
+// 4.0 TB/s of the 1.98 GB that have to move (a large copy reaches 4.8) at 0.84
+// PFLOP/s; 8 experts of 4096 rows each in 350, 1.18 PFLOP/s (a large library product
+// 1.45). A stage's copies take 0.6 to 1 us to arrive, and the bytes in flight are what
+// LDS holds: hence large blocks, one a CU, and a ring that takes all of it. The 64
+// rows of 8 tokens, 64 x 1536 x 2048, read their experts' 254 MB of weights in 52 us,
+// 4.9 TB/s.
 enum GgKind { kGgRows, kGgRowsT, kGgWeight };       // forward, input gradient, weight gradient
 
 template <int KIND, int WM, int MW, int NW, bool F32, bool ADD>
@@ -541,12 +555,13 @@ static bool gg_filled(int64_t blocks) { return blocks >= 1024 || 10 * blocks >= 
 // the experts' rows are only guessed from it. us, blocks of 256 x 256, 128 x 128
 // and 32 x 128, forward and input gradient:
 //   E x N x D        rows each
-//   128 x 4096 x 1536  256   620 579   609 569   1253 1144     8 x 4096 x 1536   4096   370 348   431 415   862 881
-//   128 x 4096 x 1536   32   301 281   305 300    334  325    64 x 1536 x 2048   128   104  84   112 109   161 169
-//    64 x 1536 x 2048   64   100  76    87  85    109  110    64 x 1536 x 2048    16    93  73    81  77    80  77
-//     8 x 1536 x 2048  256    41  37    20  24     34   40     8 x 1536 x 2048    64    32  27    19  16    13  17
-//     1 x 4096 x 4096 1024    75  81    37  38     71   79     1 x 4096 x 4096   256    72  80    32  33    22  28
-//   128 x 4096 x 1536    4 in the mean, skewed      -     -     121 133   117 129
+//   128 x 4096 x 1536  256   495 468   624 580   1143 1037     8 x 4096 x 1536   4096   376 350   440 424   890 845
+//   128 x 4096 x 1536  128   362 337   422 425    682  615   128 x 4096 x 1536     32   294 289   305 306   333 325
+//    64 x 1536 x 2048  128   105  89   114 114    166  174    64 x 1536 x 2048     64    94  79    87  86   110 114
+//    64 x 1536 x 2048   16    89  75    79  78     78   77     8 x 1536 x 2048    256    41  37    20  18    30  32
+//     8 x 1536 x 2048   64    23  21    15  16     13   12     1 x 4096 x 4096   1024    74  81    37  38    67  72
+//     1 x 4096 x 4096  256    71  79    30  32     22   24   128 x 4096 x 1536      4   133 144   120 135   116 129
+// (the last in the mean, skewed)
 static int gg_rows_blocks(int64_t rows_max, int E, int cols) {
     const auto blocks = [&](int64_t side) {         // about: half a block of rows is lost an expert
         const int64_t rows = rows_max / side + (rows_max < E ? rows_max : E) / 2, least = rows_max < E ? rows_max : E;
@@ -629,11 +644,15 @@ extern "C" int moe_grouped_gemm_wgrad(const uint16_t* d_out, int64_t d_out_row_s
     a.b = (const uint8_t*)x; a.b_stride = 2 * x_row_stride;
     a.offsets = expert_offsets; a.counts = expert_counts; a.E = E; a.R = rows_max; a.M = N; a.N = D;
     a.out = (uint8_t*)d_w; a.out_stride = (int64_t)D * (f32 ? 4 : 2); a.out_group = a.out_stride * N; a.out_vec = a.out_stride % 16 == 0;
-    // us, blocks of 256 x 256 and 128 x 128, bf16 d_w: 128 experts x 4096 x 1536, 256 rows each 664 and 774 (fp32 871
-    // and 1064), 32 rows 392 and 388, 4 rows in the mean 440 and 305; 64 x 1536 x 2048, 128 rows 133 and 124; 8 x 1536
-    // x 2048, 256 rows, 384 wide blocks on 256 CUs, 29.5 and 24.8; 8 x 4096 x 1536, 4096 rows, 350 and 438
+    // us, blocks of 256 x 256 and 128 x 128, bf16 d_w and fp32:
+    //   128 x 4096 x 1536, rows each 256   690 777   883 1065      64 x 1536 x 2048, 128   136 132   176 155
+    //                                128   527 619   716  838                         64   115 110   160 131
+    //                                 32   383 388   546  551                         16   102 100   145 120
+    //                  4 in the mean, skewed 333 303 570 566       8 x 1536 x 2048, 256    27  23    35  27
+    //     8 x 4096 x 1536,          4096   348 444   352  464       1 x 4096 x 4096, 1024   36  39    42  43
+    // (a block of few rows is its output alone, which the smaller ones write beside another's reads; not so in long runs)
     const int64_t wide = (int64_t)E * ((N + 255) / 256) * ((D + 255) / 256);
-    if (rows_max >= 192 * (int64_t)E && wide >= 200 && gg_filled(wide))
+    if (rows_max >= (wide >= 4096 ? 96 : 192) * (int64_t)E && wide >= 200 && gg_filled(wide))
         return launch_grouped<kGgWeight, 2, 4, 4>(a, f32, accumulate != 0, (hipStream_t)stream, name);
     return launch_grouped<kGgWeight, 2, 2, 2>(a, f32, accumulate != 0, (hipStream_t)stream, name);
 }
