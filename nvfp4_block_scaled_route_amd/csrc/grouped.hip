@@ -301,6 +301,38 @@ __device__ __forceinline__ void gg_store(uint8_t* out, int64_t stride, bool vec,
     }
 }
 
+// The same of fp32 rows, straight from the accumulators: there a lane holds one
+// column of 4 consecutive rows at a time, so that 32 lanes store a row's whole cache
+// line (or part of it, at any stride).
+template <int NT, bool ADD>
+__device__ __forceinline__ void gg_store32(uint8_t* out, int64_t stride, const gg_f16v (&acc)[NT], int live, int left, int cols, int lane) {
+    const int c = lane & 31, g = lane >> 5;
+    uint8_t* at = out + 4 * g * stride + 4 * c;
+    if (live >= 32 && cols >= 32 * NT) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float* row = reinterpret_cast<float*>(at + (8 * (i / 4) + i % 4) * stride);
+            float v[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) v[n] = ADD ? row[32 * n] : 0.0f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) __builtin_nontemporal_store(ADD ? __fadd_rn(acc[n][i], v[n]) : acc[n][i], row + 32 * n);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int r = 8 * (i / 4) + i % 4 + 4 * g;
+        float* row = reinterpret_cast<float*>(at + (8 * (i / 4) + i % 4) * stride);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            if (r >= left || 32 * n + c >= cols) continue;
+            const float v = r < live ? acc[n][i] : 0.0f;
+            __builtin_nontemporal_store(ADD ? __fadd_rn(v, row[32 * n]) : v, row + 32 * n);
+        }
+    }
+}
+
 // ------------------------------------------------------------------ the kernel
 // 4 waves, WM along the output's rows; a wave has MW x NW tiles of 32 x 32, its
 // tiles' rows dealt round the waves, so that a block of few rows is few tiles of
@@ -409,7 +441,8 @@ __device__ __forceinline__ void gg_block(const GgArgs& a, const GgBlock& b, uint
             };
             auto mfma = [&](const Operands& o, int i) __attribute__((always_inline)) {             // MFMA i of a step
                 if (i / NW < LIVE)
-                    acc[i / NW][i % NW] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(o.b[i % NW], o.a[i / NW], acc[i / NW][i % NW], 0, 0, 0);
+                    acc[i / NW][i % NW] = F32 ? __builtin_amdgcn_mfma_f32_32x32x16_bf16(o.a[i / NW], o.b[i % NW], acc[i / NW][i % NW], 0, 0, 0)
+                                              : __builtin_amdgcn_mfma_f32_32x32x16_bf16(o.b[i % NW], o.a[i / NW], acc[i / NW][i % NW], 0, 0, 0);
                 __builtin_amdgcn_sched_barrier(0);
             };
             __builtin_amdgcn_s_waitcnt(vmcnt_at_most((R::kRing - 1) * kAll));
@@ -458,8 +491,9 @@ __device__ __forceinline__ void gg_block(const GgArgs& a, const GgBlock& b, uint
             if (r0 >= left || c0 >= a.N) continue;
             uint8_t* out = a.out + (KIND == kGgWeight ? b.e * a.out_group + (m0 + r0) * a.out_stride
                                                       : (b.row + (int64_t)m0 + r0) * a.out_stride);
-            gg_store<NW, F32, ADD>(out + (int64_t)c0 * (F32 ? 4 : 2), a.out_stride, a.out_vec, slab, acc[m], live - r0, left - r0,
-                                   a.N - c0, lane);
+            out += (int64_t)c0 * (F32 ? 4 : 2);
+            if constexpr (F32) gg_store32<NW, ADD>(out, a.out_stride, acc[m], live - r0, left - r0, a.N - c0, lane);
+            else gg_store<NW, F32, ADD>(out, a.out_stride, a.out_vec, slab, acc[m], live - r0, left - r0, a.N - c0, lane);
             __builtin_amdgcn_sched_barrier(0);
         }
         // rows of padding behind those tiles: whole pieces of 16 bytes (N % 8 == 0) where rows start at such
