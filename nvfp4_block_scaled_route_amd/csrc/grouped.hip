@@ -144,7 +144,7 @@ __device__ __forceinline__ int xcd_run(int total) {
 __device__ __forceinline__ int gg_split(GgBlock& g, int bm) {
     const int held = (g.rows + bm - 1) / bm, all = (g.end - g.row + bm - 1 - bm / 2) / bm;
     g.tiles = g.end == g.row ? 0 : held > all ? held : all > 1 ? all : 1;
-    g.side = held > 1 && held == g.tiles ? ((g.rows + held - 1) / held + 15) & ~15 : bm;
+    g.side = held > 1 && held == g.tiles ? ((g.rows - 1) / held + 16) & ~15 : bm;
     return held;
 }
 
@@ -179,20 +179,24 @@ __device__ __forceinline__ bool gg_find(const GgArgs& a, GgBlock& out, uint8_t* 
         gg_shape<BM, BN, TALL>(a.N, g);
         mine += g.tiles * g.nt;
     }
+    mine = mine < a.blocks ? mine : a.blocks;       // (a.blocks <= 2^24: a wave's sum stays in 31 bits)
     const int upto = wave_inclusive_scan(mine);
     if (lane == 63) s_sum[wave] = upto;
     if (tid == 0) s_out.e = -1;
     __syncthreads();
-    int before = upto - mine, total = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
-    for (int w = 0; w < wave; ++w) before += s_sum[w];
-    const int id = xcd_run(total < a.blocks ? total : a.blocks);
+    int64_t before = upto - mine, total = 0;
+    for (int w = 0; w < 4; ++w) {
+        if (w < wave) before += s_sum[w];
+        total += s_sum[w];
+    }
+    const int id = xcd_run((int)(total < a.blocks ? total : a.blocks));
     if (id < 0) return false;
     if (id >= before && id < before + mine) {
         for (int e = e0; e < e0 + per && e < a.E; ++e) {
             GgBlock g;
             gg_rows(a, e, g);
             gg_shape<BM, BN, TALL>(a.N, g);
-            g.tile = id - before;
+            g.tile = (int)(id - before);
             if (id >= before && id < before + g.tiles * g.nt) s_out = g;
             before += g.tiles * g.nt;
         }
