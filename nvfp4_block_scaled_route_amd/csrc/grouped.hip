@@ -348,8 +348,8 @@ __device__ __forceinline__ void gg_store32(uint8_t* out, int64_t stride, const g
 // PFLOP/s; 8 experts of 4096 rows each in 350, 1.18 PFLOP/s (a large library product
 // 1.45). A stage's copies take 0.6 to 1 us to arrive, and the bytes in flight are what
 // LDS holds: hence large blocks, one a CU, and a ring that takes all of it. The 64
-// rows of 8 tokens, 64 x 1536 x 2048, read their experts' 254 MB of weights in 52 us,
-// 4.9 TB/s.
+// rows of 8 tokens, 64 x 1536 x 2048, read their experts' 254 MB of weights in 48 us,
+// 5.3 TB/s.
 enum GgKind { kGgRows, kGgRowsT, kGgWeight };       // forward, input gradient, weight gradient
 
 template <int KIND, int WM, int MW, int NW, bool F32, bool ADD>
@@ -418,8 +418,16 @@ __device__ __forceinline__ void gg_block(const GgArgs& a, const GgBlock& b, uint
         constexpr int LIVE = decltype(tiles)::value;
         using R = typename S::template Ring<LIVE>;
         constexpr int kAll = R::kAll;
+        // Rows whose length is a multiple of some KB meet in few memory channels at one place along them: forward, where both
+        // operands are read along their rows, blocks begin at different stages and go round (D = 2048: 8 tokens' rows 57 ->
+        // 48 us, 128 rows an expert 107 -> 98; 1536, 256 rows: 497 -> 489), by expert and columns. The gradients gain nothing by it.
+        const int start = KIND == kGgRows && stages > 0 ? (int)((unsigned)(b.e * nt + n0 / S::kBN) % (unsigned)stages) : 0;
         auto copy = [&](int s, int q0, int q1) __attribute__((always_inline)) {        // copies [q0, q1) of stage s
             const uint32_t at = lds0 + (s % R::kRing) * R::kStage;
+            if (KIND == kGgRows && s < stages) {
+                s += start;
+                if (s >= stages) s -= stages;
+            }
 #pragma unroll
             for (int q = q0; q < q1; ++q) {
                 if (q < R::kCopiesA) ca.issue(at, s, q, wave);
@@ -594,12 +602,12 @@ static bool gg_filled(int64_t blocks) { return blocks >= 1024 || 10 * blocks >= 
 // the experts' rows are only guessed from it. us, blocks of 256 x 256, 128 x 128
 // and 32 x 128, forward and input gradient:
 //   E x N x D        rows each
-//   128 x 4096 x 1536  256   495 468   624 580   1143 1037     8 x 4096 x 1536   4096   376 350   440 424   890 845
-//   128 x 4096 x 1536  128   362 337   422 425    682  615   128 x 4096 x 1536     32   294 289   305 306   333 325
-//    64 x 1536 x 2048  128   105  89   114 114    166  174    64 x 1536 x 2048     64    94  79    87  86   110 114
-//    64 x 1536 x 2048   16    89  75    79  78     78   77     8 x 1536 x 2048    256    41  37    20  18    30  32
-//     8 x 1536 x 2048   64    23  21    15  16     13   12     1 x 4096 x 4096   1024    74  81    37  38    67  72
-//     1 x 4096 x 4096  256    71  79    30  32     22   24   128 x 4096 x 1536      4   133 144   120 135   116 129
+//   128 x 4096 x 1536  256   536 493   628 583   1149 1045     8 x 4096 x 1536   4096   376 354   443 434   909 858
+//   128 x 4096 x 1536  128   345 324   423 421    679  618   128 x 4096 x 1536     32   294 289   307 307   334 326
+//    64 x 1536 x 2048  128    98  92   112 115    168  170    64 x 1536 x 2048     64    85  79    83  86   110 111
+//    64 x 1536 x 2048   16    77  75    72  78     72   77     8 x 1536 x 2048    256    41  36    21  18    31  32
+//     8 x 1536 x 2048   64    23  22    15  16     14   13     1 x 4096 x 4096   1024    74  81    37  38    65  73
+//     1 x 4096 x 4096  256    72  77    31  32     23   25   128 x 4096 x 1536      4   132 145   120 134   116 129
 // (the last in the mean, skewed)
 static int gg_rows_blocks(int64_t rows_max, int E, int cols) {
     const auto blocks = [&](int64_t side) {         // about: half a block of rows is lost an expert
