@@ -216,19 +216,17 @@ __device__ __forceinline__ bool gg_find(const GgArgs& a, GgBlock& out, uint8_t* 
 }
 
 // ------------------------------------------------------------------ output
-// 32 rows x NT tiles of 32 columns of a wave's block, turned in the wave's own part
-// of the LDS: a lane holds 4 consecutive columns of one row at a time, and whole
+// 32 rows x NT tiles of 32 columns of a wave's block, bf16, turned in the wave's own
+// part of the LDS: a lane holds 4 consecutive columns of one row at a time, and whole
 // 16-byte pieces of the rows are stored. Of `left` rows, those from `live` on are
-// zeros. ADD: added to what the output holds, in fp32, rounded once.
-template <int NT, bool F32>
-constexpr int gg_row_bytes() { return 32 * NT * (F32 ? 4 : 2) + 16; }
+// zeros. ADD: added to what the output holds, in fp32 (in the LDS too), rounded once.
+template <int NT, bool ADD>
+constexpr int gg_row_bytes() { return 32 * NT * (ADD ? 4 : 2) + 16; }
 
-template <int NT, bool F32, bool ADD>
+template <int NT, bool ADD>
 __device__ __forceinline__ void gg_store(uint8_t* out, int64_t stride, bool vec, uint8_t* slab, const gg_f16v (&acc)[NT],
                                          int live, int left, int cols, int lane) {
-    constexpr bool kWide = F32 || ADD;      // fp32 in LDS
-    constexpr int kRow = gg_row_bytes<NT, kWide>(), kEs = F32 ? 4 : 2, kPiece = 16 / kEs, kPieces = 32 * NT / kPiece;
-    constexpr int kCount = kPieces / 2, kBatch = kCount < 8 ? kCount : kCount / 2;
+    constexpr int kRow = gg_row_bytes<NT, ADD>(), kPieces = 4 * NT, kCount = kPieces / 2, kBatch = kCount < 8 ? kCount : kCount / 2;
     static_assert(kCount % kBatch == 0, "whole batches");
     const int r = lane & 31, g = lane >> 5;
     const bool zero = r >= live;
@@ -241,28 +239,24 @@ __device__ __forceinline__ void gg_store(uint8_t* out, int64_t stride, bool vec,
             const gg_f16v& a = acc[n];
             const float v0 = zero ? 0.0f : a[4 * q], v1 = zero ? 0.0f : a[4 * q + 1];
             const float v2 = zero ? 0.0f : a[4 * q + 2], v3 = zero ? 0.0f : a[4 * q + 3];
-            if constexpr (kWide) *reinterpret_cast<floatx4*>(slab + r * kRow + c * 4) = floatx4{v0, v1, v2, v3};
+            if constexpr (ADD) *reinterpret_cast<floatx4*>(slab + r * kRow + c * 4) = floatx4{v0, v1, v2, v3};
             else *reinterpret_cast<uint2*>(slab + r * kRow + c * 2) = make_uint2(bf16x2_pack(v0, v1), bf16x2_pack(v2, v3));
         }
     wave_lds_sync();
     // piece lane + 64 j of the rows' in order: where 64 are whole rows, from j to j the same rows further down
     constexpr bool kEven = 64 % kPieces == 0;
     constexpr int kRowsPer = kEven ? 64 / kPieces : 0;
-    const int lane_row = lane / kPieces, lane_col = lane % kPieces * kPiece;
+    const int lane_row = lane / kPieces, lane_col = lane % kPieces * 8;
     const auto row = [&](int j) { return kEven ? lane_row + j * kRowsPer : (lane + 64 * j) / kPieces; };
-    const auto col = [&](int j) { return kEven ? lane_col : (lane + 64 * j) % kPieces * kPiece; };
-    const uint8_t* src0 = slab + lane_row * kRow + lane_col * (kWide ? 4 : 2);
-    uint8_t* dst0 = out + lane_row * stride + lane_col * kEs;
-    const auto src = [&](int j) { return kEven ? src0 + j * kRowsPer * kRow : slab + row(j) * kRow + col(j) * (kWide ? 4 : 2); };
-    const auto dst = [&](int j) { return kEven ? dst0 + j * kRowsPer * stride : out + row(j) * stride + col(j) * kEs; };
+    const auto col = [&](int j) { return kEven ? lane_col : (lane + 64 * j) % kPieces * 8; };
+    const uint8_t* src0 = slab + lane_row * kRow + lane_col * (ADD ? 4 : 2);
+    uint8_t* dst0 = out + lane_row * stride + lane_col * 2;
+    const auto src = [&](int j) { return kEven ? src0 + j * kRowsPer * kRow : slab + row(j) * kRow + col(j) * (ADD ? 4 : 2); };
+    const auto dst = [&](int j) { return kEven ? dst0 + j * kRowsPer * stride : out + row(j) * stride + col(j) * 2; };
     // a piece of the output: what LDS holds, or that and the output's own
     const auto piece = [](const uint8_t* p, u32x4 old) {
         if constexpr (!ADD) {
             return *reinterpret_cast<const u32x4*>(p);
-        } else if constexpr (F32) {
-            const floatx4 v = *reinterpret_cast<const floatx4*>(p);
-            return u32x4{__float_as_uint(__fadd_rn(v[0], __uint_as_float(old[0]))), __float_as_uint(__fadd_rn(v[1], __uint_as_float(old[1]))),
-                         __float_as_uint(__fadd_rn(v[2], __uint_as_float(old[2]))), __float_as_uint(__fadd_rn(v[3], __uint_as_float(old[3])))};
         } else {
             u32x4 o;
 #pragma unroll
@@ -292,20 +286,17 @@ __device__ __forceinline__ void gg_store(uint8_t* out, int64_t stride, bool vec,
     for (int j = 0; j < kCount; ++j) {
         const int c = col(j);
         if (row(j) >= left || c >= cols) continue;
-        if (vec && c + kPiece <= cols) {
+        if (vec) {          // (columns come in eights: whole pieces)
             u32x4 old = {};
             if constexpr (ADD) old = *reinterpret_cast<const u32x4*>(dst(j));
             __builtin_nontemporal_store(piece(src(j), old), reinterpret_cast<u32x4*>(dst(j)));
-        } else if constexpr (!ADD) {        // rows at any stride; d_w's are contiguous, whole pieces
-            for (int k = 0; k < kPiece && c + k < cols; ++k) {
-                if constexpr (F32) reinterpret_cast<float*>(dst(j))[k] = reinterpret_cast<const float*>(src(j))[k];
-                else reinterpret_cast<uint16_t*>(dst(j))[k] = reinterpret_cast<const uint16_t*>(src(j))[k];
-            }
+        } else if constexpr (!ADD) {        // rows at any stride; d_w's are contiguous
+            for (int k = 0; k < 8; ++k) reinterpret_cast<uint16_t*>(dst(j))[k] = reinterpret_cast<const uint16_t*>(src(j))[k];
         }
     }
 }
 
-// The same of fp32 rows, straight from the accumulators: there a lane holds one
+// The same of fp32, straight from the accumulators: there a lane holds one
 // column of 4 consecutive rows at a time, so that 32 lanes store a row's whole cache
 // line (or part of it, at any stride). Weight gradient of 128 experts x 4096 x 1536,
 // 256 rows each: 892 -> 813 us.
@@ -357,7 +348,7 @@ struct GgShape {
     static constexpr int kWN = 4 / WM, kBM = 32 * WM * MW, kBN = 32 * kWN * NW;
     using A = std::conditional_t<KIND == kGgWeight, Across<kBM>, Along<kBM>>;
     using B = std::conditional_t<KIND == kGgRows, Along<kBN>, Across<kBN>>;
-    static constexpr int kSlab = 32 * gg_row_bytes<NW, F32 || ADD>();
+    static constexpr int kSlab = F32 ? 0 : 32 * gg_row_bytes<NW, ADD>();
     static constexpr bool kTall = KIND != kGgWeight && MW * NW == 16;     // beside tall blocks
     static constexpr int kPerCu = MW * NW >= 12 ? 1 : 2, kLds = 160 * 1024 / kPerCu;
     // A ring of stages for a block of LIVE row tiles a wave: what such a block does not need makes room for more of them.
@@ -506,7 +497,7 @@ __device__ __forceinline__ void gg_block(const GgArgs& a, const GgBlock& b, uint
                                                       : (b.row + (int64_t)m0 + r0) * a.out_stride);
             out += (int64_t)c0 * (F32 ? 4 : 2);
             if constexpr (F32) gg_store32<NW, ADD>(out, a.out_stride, acc[m], live - r0, left - r0, a.N - c0, lane);
-            else gg_store<NW, F32, ADD>(out, a.out_stride, a.out_vec, slab, acc[m], live - r0, left - r0, a.N - c0, lane);
+            else gg_store<NW, ADD>(out, a.out_stride, a.out_vec, slab, acc[m], live - r0, left - r0, a.N - c0, lane);
             __builtin_amdgcn_sched_barrier(0);
         }
         // rows of padding behind those tiles: whole pieces of 16 bytes (N % 8 == 0) where rows start at such
