@@ -191,14 +191,17 @@ class Fp8Linear:
 
 class Routing:
     """A routing of T tokens to K of E experts: what moe_route writes, and its fields
-    as the calls on sorted rows take them."""
+    as the calls on sorted rows take them. `stream` clears the metadata and owns the
+    buffers: a call on another stream is ordered behind it, and ends before the last
+    reference to the Routing goes, by the caller's order (as with MxLinear)."""
 
-    def __init__(self, T: int, K: int, E: int, tile_m: int, device="cuda"):
+    def __init__(self, T: int, K: int, E: int, tile_m: int, device="cuda", stream=None):
         self.T, self.K, self.E, self.tile_m = T, K, E, tile_m
         self.layout = N.moe_meta_layout_get(T, K, E, tile_m)
-        self.meta = torch.full((self.layout.total_ints,), -1, dtype=torch.int32, device=device)
-        self.ids = torch.empty((T, K), dtype=torch.int32, device=device)
-        self.weights = torch.empty((T, K), dtype=torch.float32, device=device)
+        with _owner(stream):
+            self.meta = torch.full((self.layout.total_ints,), -1, dtype=torch.int32, device=device)
+            self.ids = torch.empty((T, K), dtype=torch.int32, device=device)
+            self.weights = torch.empty((T, K), dtype=torch.float32, device=device)
         L = self.layout
 
         def field(at, length):
@@ -225,17 +228,18 @@ class ExpertMlp:
     forward keeps what backward needs in this object's buffers, and backward uses
     them up: a backward belongs to the last forward, on the same routing, and calls
     that share one ExpertMlp must not overlap. Nothing is allocated per call, so
-    they can be captured."""
+    they can be captured. `stream` owns the buffers, as a Routing's does its."""
 
-    def __init__(self, T: int, K: int, E: int, H: int, I: int, tile_m: int, device="cuda"):
+    def __init__(self, T: int, K: int, E: int, H: int, I: int, tile_m: int, device="cuda", stream=None):
         self.T, self.K, self.E, self.H, self.I = T, K, E, H, I
         R = self.R = N.moe_rows_max(T, K, E, tile_m)
 
         def rows(width):
             return torch.empty((R, width), dtype=torch.bfloat16, device=device)
 
-        self.rows, self.gate_up, self.inter, self.out_rows = rows(H), rows(2 * I), rows(I), rows(H)
-        self.d_inter, self.d_rows = rows(I), rows(H)
+        with _owner(stream):
+            self.rows, self.gate_up, self.inter, self.out_rows = rows(H), rows(2 * I), rows(I), rows(H)
+            self.d_inter, self.d_rows = rows(I), rows(H)
         self._kept = False
 
     def forward(self, x, routing: Routing, w13, w2, out, stream=None) -> None:
