@@ -244,6 +244,7 @@ class ExpertMlp:
 
     def forward(self, x, routing: Routing, w13, w2, out, stream=None) -> None:
         """out bf16 [T, H]."""
+        self._kept = False      # also where a call below raises
         r = routing
         N.moe_dispatch(x, r.exp2perm, r.perm2tok, r.total_rows, self.rows, stream)
         N.moe_grouped_gemm(self.rows, w13, r.expert_offsets, r.expert_counts, self.gate_up, stream)
