@@ -197,6 +197,7 @@ class Routing:
 
     def __init__(self, T: int, K: int, E: int, tile_m: int, device="cuda", stream=None):
         self.T, self.K, self.E, self.tile_m = T, K, E, tile_m
+        self.runs = 0       # calls so far
         self.layout = N.moe_meta_layout_get(T, K, E, tile_m)
         with _owner(stream):
             self.meta = torch.full((self.layout.total_ints,), -1, dtype=torch.int32, device=device)
@@ -214,6 +215,7 @@ class Routing:
         self.expert_counts = field(L.expert_counts, E)
 
     def __call__(self, logits, expert_bias=None, is_padding=None, route_scale: float = 1.0, stream=None) -> None:
+        self.runs += 1
         N.moe_route(logits, expert_bias, is_padding, self.K, route_scale, self.tile_m, 0, self.E, self.ids, self.weights,
                     self.meta, stream)
 
@@ -226,9 +228,11 @@ class ExpertMlp:
     norms each row). w13 bf16 [E, 2 I, H], gate rows first, w2 bf16 [E, H, I].
 
     forward keeps what backward needs in this object's buffers, and backward uses
-    them up: a backward belongs to the last forward, on the same routing, and calls
-    that share one ExpertMlp must not overlap. Nothing is allocated per call, so
-    they can be captured. `stream` owns the buffers, as a Routing's does its."""
+    them up: a backward belongs to the last forward, on the same routing, which has not
+    run again in between (another one is refused; replays of captured calls are not
+    counted, their order is the caller's), and calls that share one ExpertMlp must not
+    overlap. Nothing is allocated per call, so they can be captured. `stream` owns the
+    buffers, as a Routing's does its."""
 
     def __init__(self, T: int, K: int, E: int, H: int, I: int, tile_m: int, device="cuda", stream=None):
         self.T, self.K, self.E, self.H, self.I = T, K, E, H, I
@@ -240,27 +244,31 @@ class ExpertMlp:
         with _owner(stream):
             self.rows, self.gate_up, self.inter, self.out_rows = rows(H), rows(2 * I), rows(I), rows(H)
             self.d_inter, self.d_rows = rows(I), rows(H)
-        self._kept = False
+        self._kept = None       # the forward's routing and the run of it
 
     def forward(self, x, routing: Routing, w13, w2, out, stream=None) -> None:
         """out bf16 [T, H]."""
-        self._kept = False      # also where a call below raises
+        self._kept = None       # also where a call below raises
         r = routing
         N.moe_dispatch(x, r.exp2perm, r.perm2tok, r.total_rows, self.rows, stream)
         N.moe_grouped_gemm(self.rows, w13, r.expert_offsets, r.expert_counts, self.gate_up, stream)
         N.moe_swiglu(self.gate_up, r.perm2tok, r.total_rows, self.inter, stream)
         N.moe_grouped_gemm(self.inter, w2, r.expert_offsets, r.expert_counts, self.out_rows, stream)
         N.moe_combine(self.out_rows, r.exp2perm, r.weights, out, stream)
-        self._kept = True
+        self._kept = r, r.runs
 
     def backward(self, d_out, routing: Routing, w13, w2, d_x, d_w13, d_w2, d_weights, accumulate: bool = False,
                  stream=None) -> None:
         """From d_out bf16 [T, H]: d_x bf16 [T, H], d_w13 and d_w2 (bf16 or fp32, added to
         with accumulate) and d_weights fp32 [T, K]."""
-        if not self._kept:
+        if self._kept is None:
             raise ValueError("a backward without its forward")
-        self._kept = False
-        r = routing
+        r, runs = self._kept
+        if routing is not r:
+            raise ValueError("a backward on another routing than its forward's")
+        if r.runs != runs:
+            raise ValueError("the routing ran again since the forward")
+        self._kept = None
         d_rows2, d_gate_up = self.out_rows, self.gate_up        # in place
         N.moe_combine_bwd(d_out, self.out_rows, r.exp2perm, r.perm2tok, r.total_rows, r.weights, d_rows2, d_weights, stream)
         N.moe_grouped_gemm_wgrad(d_rows2, self.inter, r.expert_offsets, r.expert_counts, d_w2, accumulate, stream)

@@ -60,3 +60,44 @@ def test_a_forward_that_raises_leaves_nothing_to_go_back_from(done, monkeypatch)
     assert len(p.calls) == before
     p.forward()
     p.backward()
+
+
+def test_a_routing_that_ran_again_is_refused(monkeypatch):
+    """Its maps are no longer those of the rows that the forward kept; with a new forward
+    they are."""
+    p = Program(monkeypatch)
+    p.route()
+    p.forward()
+    p.route()
+    before = len(p.calls)
+    with pytest.raises(ValueError, match="ran again"):
+        p.backward()
+    assert len(p.calls) == before
+    p.forward()
+    p.backward()
+
+
+def test_a_routing_that_was_refused_midway_is_refused(monkeypatch):
+    p = Program(monkeypatch)
+    p.route()
+    p.forward()
+    p.fails = len(p.calls)
+    with pytest.raises(ValueError, match="refused"):
+        p.route()
+    p.fails = None
+    with pytest.raises(ValueError, match="ran again"):
+        p.backward()
+
+
+def test_another_routing_is_refused(monkeypatch):
+    """And the forward's own is taken after that."""
+    p = Program(monkeypatch)
+    other = LY.Routing(5, 2, 4, 16, "cpu")
+    p.route()
+    other(torch.zeros(5, 4))
+    p.forward()
+    before = len(p.calls)
+    with pytest.raises(ValueError, match="forward's"):
+        p.backward(other)
+    assert len(p.calls) == before
+    p.backward()
