@@ -293,12 +293,18 @@ class LayerShape:
 class Buffers:
     """Every device buffer one layer call writes, sized once by moe_workspace_bytes
     and carved from one allocation (nothing is allocated per call, so the calls
-    can be captured in a HIP graph)."""
+    can be captured in a HIP graph). `stream` clears the metadata and owns the buffers:
+    a call on another stream is ordered behind it, and ends before the last reference
+    to the Buffers goes, by the caller's order (as with MxLinear)."""
 
-    def __init__(self, shape: LayerShape, device="cuda"):
+    def __init__(self, shape: LayerShape, device="cuda", stream=None):
         s = self.shape = shape
         L = self.layout = N.moe_meta_layout_get(s.T, s.K, s.E, s.tile_m)
         W = self.ws_layout = N.moe_workspace_bytes(s.T, s.K, s.E, s.H, s.I, s.tile_m, s.tp)
+        with _owner(stream):
+            self._allocate(s, L, W, device)
+
+    def _allocate(self, s, L, W, device) -> None:
         self.workspace = torch.empty((W.total_bytes,), dtype=torch.uint8, device=device)
         rm, I_slice = L.rows_max, s.I // s.tp
 

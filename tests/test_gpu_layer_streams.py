@@ -1,11 +1,13 @@
 """Objects of the layer module made and called on a stream of their own while the current
 one is busy: nothing that they do waits for it, and nothing of its comes late into them."""
+import numpy as np
 import pytest
 import torch
 
 from nvfp4_block_scaled_route_amd import layer as LY
+from nvfp4_block_scaled_route_amd import workloads as W
 
-from .gpu_common import DEV, say
+from .gpu_common import DEV, dev, host, say, upload_weights
 from .test_gpu_expert_mlp import Step
 
 pytestmark = pytest.mark.gpu
@@ -46,3 +48,40 @@ def test_routing_and_experts_on_a_stream_of_their_own(raw):
     r = s.routing
     for a, b in zip((r.exp2perm, r.perm2tok[:total], r.expert_offsets, r.expert_counts), maps):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_buffers_on_a_stream_of_their_own(raw):
+    """The layer's, in the same way."""
+    wl = W.WORKLOADS["tiny"]
+    inp = W.make_inputs(wl)
+    w = upload_weights(inp)
+    x, gs, lg, nw = dev(inp.x_bf16), dev(inp.a1_gscale), dev(inp.logits), dev(inp.norm_weight_bf16)
+    shape = LY.LayerShape(wl.T, wl.H, wl.I, wl.E, wl.K, wl.tile_m)
+
+    def run(bufs, stream=None):
+        LY.run_layer(bufs, x, gs, lg, None, None, w, nw, wl.gain_center, wl.eps, bool(wl.weight_before_norm), stream=stream)
+
+    first = LY.Buffers(shape, DEV)
+    run(first)
+    torch.cuda.synchronize()
+    want, size = {k: host(getattr(first, k)).copy() for k in ("ids", "weights", "meta", "out")}, first.workspace.nbytes
+    first.check_sync()
+    del first
+    side, done = torch.cuda.Stream(), torch.cuda.Event()
+    torch.cuda.synchronize()
+    say("Buffers on a side stream, raw", raw)
+    junk = torch.empty(size, dtype=torch.uint8, device=DEV)
+    torch.cuda._sleep(60_000_000)
+    junk.fill_(0xFF)
+    done.record()
+    del junk
+    handle = side.cuda_stream if raw else side
+    bufs = LY.Buffers(shape, DEV, stream=handle)
+    run(bufs, handle)
+    side.synchronize()
+    say("the current stream has ended before it:", done.query())
+    torch.cuda.synchronize()
+    bufs.check_sync()
+    for k, v in want.items():
+        assert np.array_equal(host(getattr(bufs, k)), v), k

@@ -8,7 +8,9 @@ import torch
 from nvfp4_block_scaled_route_amd import layer as LY
 
 MADE = {"Routing": lambda stream: LY.Routing(5, 2, 4, 16, "cpu", stream),
-        "ExpertMlp": lambda stream: LY.ExpertMlp(5, 2, 4, 64, 24, 16, "cpu", stream)}
+        "ExpertMlp": lambda stream: LY.ExpertMlp(5, 2, 4, 64, 24, 16, "cpu", stream),
+        "Buffers": lambda stream: LY.Buffers(LY.LayerShape(5, 64, 64, 4, 2, 16), "cpu", stream),
+        "Buffers of no rows": lambda stream: LY.Buffers(LY.LayerShape(0, 64, 64, 4, 2, 16), "cpu", stream)}
 
 
 @pytest.mark.parametrize("kind", MADE)
