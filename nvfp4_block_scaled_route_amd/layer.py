@@ -61,15 +61,18 @@ def slice_weights(full: N.Weights, r: int, tp: int, H: int, I: int) -> N.Weights
         w2_offset=full.w2_offset + t2 * 1024, w2_sf_offset=full.w2_sf_offset + t2 * 128)
 
 
+def _stream(stream):
+    """A stream object or a raw stream's number (0: the default stream) -> the object."""
+    if isinstance(stream, int):
+        return torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return stream
+
+
 def _owner(stream):
     """The context in which buffers that `stream` owns are allocated: memory that
     another stream freed may still be written by the work in front of the free.
     None: the current stream."""
-    if stream is None:
-        return contextlib.nullcontext()
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-    return torch.cuda.stream(stream)
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(_stream(stream))
 
 
 class MxLinear:
@@ -86,16 +89,12 @@ class MxLinear:
         n, k = weight_bf16.shape
         N.mx_gemm_validate(a_fmt, w_fmt, n, k)      # here, not at the first call
         self.N, self.K, self.max_tokens, self.w_fmt, self.a_fmt = n, k, max_tokens, w_fmt, a_fmt
-        # allocated on that stream: memory that another one freed may still be
-        # written by the work in front of the free
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        with _owner(stream):
             self.w_codes, self.w_sf = self._buffers(n, w_fmt, weight_bf16.device)
             self.a_codes, self.a_sf = self._buffers(max_tokens, a_fmt, weight_bf16.device)
         N.mx_quant(weight_bf16, w_fmt, self.w_codes, self.w_sf, stream)
         if stream is not None:      # the caller may drop the weight while that stream still reads it
-            weight_bf16.record_stream(stream)
+            weight_bf16.record_stream(_stream(stream))
 
     def _buffers(self, rows, fmt, device):
         width = self.K // 2 if fmt == N.MOE_MX_E2M1 else self.K
@@ -160,9 +159,7 @@ class Fp8Linear:
             raise ValueError(f"a weight of {tuple(weight_bf16.shape)}, not {(self.N, self.K)}")
         N.fp8_quant_weight(weight_bf16, self.w_codes, self.w_sf, self.wt_codes, self.wt_sf, stream)
         if stream is not None:      # the caller may drop the weight while that stream still reads it
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-            weight_bf16.record_stream(stream)
+            weight_bf16.record_stream(_stream(stream))
 
     def _product(self, x, w_codes, w_sf, out, stream):
         T, K = x.shape
