@@ -85,3 +85,58 @@ def test_buffers_on_a_stream_of_their_own(raw):
     bufs.check_sync()
     for k, v in want.items():
         assert np.array_equal(host(getattr(bufs, k)), v), k
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_every_call_runs_on_the_stream_given(raw):
+    """Two layers on two streams, with new inputs each time, everything that the calls write
+    set to NaN or -1 before, and the current stream busy until they are done: a call that
+    went there instead would come too late, and one that wrote nothing leave NaN."""
+    steps = [Step(64, 4, 8, 136, 72, 32, seed=51), Step(300, 2, 4, 128, 264, 128, seed=52)]
+    sides, done = [torch.cuda.Stream() for _ in steps], torch.cuda.Event()
+    inputs = ("x", "d_out", "logits", "w13", "w2")
+
+    def run(s, stream=None):
+        s.forward(stream)
+        s.backward(stream=stream)
+
+    def written(s):
+        m, r = s.mlp, s.routing
+        return (s.out, s.d_x, s.d_w13, s.d_w2, s.d_weights, m.rows, m.gate_up, m.inter, m.out_rows, m.d_inter, m.d_rows, r.weights)
+
+    before = [None, None]
+    for it in range(3):
+        want = []
+        for i, s in enumerate(steps):
+            g = torch.Generator(device=DEV)
+            g.manual_seed(100 + 10 * it + i)
+            for name in inputs:
+                t = getattr(s, name)
+                scale = t.shape[-1] ** -0.5 if name.startswith("w") else 1.0
+                t.copy_(scale * torch.randn(t.shape, generator=g, device=DEV))
+            run(s)
+            want.append(s.results())
+            if before[i] is not None:
+                assert not any(torch.equal(a, b) for a, b in zip(want[i], before[i]))
+            before[i] = want[i]
+            for t in written(s):
+                t.fill_(float("nan"))
+            s.routing.meta.fill_(-1)
+            s.routing.ids.fill_(-1)
+        torch.cuda.synchronize()
+        say("two layers on two streams, raw", raw, "time", it)
+        torch.cuda._sleep(60_000_000)
+        done.record()
+        for s, side in zip(steps, sides):
+            run(s, side.cuda_stream if raw else side)
+        got = []
+        for s, side in zip(steps, sides):
+            with torch.cuda.stream(side):
+                got.append([t.clone() for t in (s.out, s.d_x, s.d_w13, s.d_w2, s.d_weights)])
+        for side in sides:
+            side.synchronize()
+        say("the current stream has ended before them:", done.query())
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            for a, b in zip(g, w):
+                assert torch.equal(a, b)
