@@ -74,8 +74,8 @@ struct FqArgs {
 };
 
 // A lane owns 8 values, 16 lanes a block; a workgroup 16 rows of one column of
-// blocks, whose scales lie side by side. HBM-bound: 4096 x 4096 in 10.6 us, 4.8 TB/s,
-// as a large copy.
+// blocks, whose scales lie side by side. HBM-bound: 4096 x 4096 in 10.6 to 11.2 us,
+// 4.5 to 4.8 TB/s, as a large copy.
 __global__ void __launch_bounds__(256) fp8_quant_kernel(FqArgs a) {
     const int64_t rows = blockIdx.x / a.blocks;
     const int b = (int)(blockIdx.x - rows * a.blocks), lane16 = threadIdx.x & 15;
@@ -112,7 +112,7 @@ __device__ __forceinline__ void transpose4(uint32_t (&w)[4]) {
 
 // A workgroup a block of 128 x 128, a thread 8 x 8 of it in registers from the
 // load to the codes; the transposed ones go through LDS to whole rows. HBM-bound:
-// 4096 x 4096 with both outputs in 14.1 us, 4.8 TB/s.
+// 4096 x 4096 with both outputs in 14.1 to 15.3 us, 4.4 to 4.8 TB/s.
 __global__ void __launch_bounds__(256) fp8_quant_weight_kernel(FwArgs a) {
     constexpr int kRow = 128 + 16;
     __shared__ __align__(16) uint8_t s_t[128 * kRow];
@@ -177,8 +177,13 @@ __global__ void __launch_bounds__(256) fp8_quant_weight_kernel(FwArgs a) {
 
 // ------------------------------------------------------------------ product
 // A block of K is one 16 x 16 x 128 MFMA, from zero; its sum is added to the
-// accumulators under its scale, a's times w's, in fp32. With the weights as the
-// MFMA's rows a lane holds 4 columns of one token (lane & 15), all under one scale.
+// accumulators under its scale, a's times w's, in fp32. Inside the block the matrix unit
+// cuts each product to 13 bits below the largest of its 8, 1.5e-5 of a result: 2% of the
+// bf16 outputs are the neighbours of the exact result's rounding (0.07% with sums in
+// fp32), and the error of all against 64 bits is that rounding's, 1.662e-3 of the norm
+// for 1.661e-3. Exact products would need bf16 operands, at half the matrix unit's rate.
+// With the weights as the MFMA's rows a lane holds 4 columns of one token (lane & 15),
+// all under one scale.
 // A lane's operand is 16 bytes at element 16 g and 16 at 64 + 16 g, g = lane / 16.
 typedef int fp_i8 __attribute__((ext_vector_type(8)));
 
@@ -358,7 +363,7 @@ struct FgShape {
 // where the blocks are fewer than the CUs a second group of waves takes half of K
 // (256 x 4096 x 4096 13.2 -> 10.9 us). 512 x 4096 x 4096 in 14.9 us: 1.15 PFLOP/s; rows
 // that start inside a cache line cost their copies twice the lines (517 x 2088, K =
-// 4096 14.4 us, K = 4112 18.1).
+// 4096 13.9 us, K = 4112 18.1).
 template <int MW, int NW, int NB, int KS>
 __global__ void __launch_bounds__(256 * KS, 2) fp8_gemm_kernel(FgArgs a) {
     using S = FgShape<MW, NW, NB, KS>;
@@ -515,8 +520,11 @@ __global__ void __launch_bounds__(256 * KS, 2) fp8_gemm_kernel(FgArgs a) {
 // to 3 the first part and the others the second, and either has two half steps to
 // arrive. The tokens' scales have 4 buffers.
 //
-// A SIMD's MFMA takes 32 cycles and the 4 additions of its sum 16, which do not run
-// beside it: 2/3 of the matrix unit's rate is the most.
+// A SIMD's MFMA takes 32 cycles. A wave that has the matrix unit to itself, as the
+// turns have it, issues one with the 4 additions of its sum in 41 (two waves at once take
+// 35 each, as one's additions run beside the other's MFMA): 84 thousand of the 122
+// thousand cycles that a CU is busy with 4096^3. The rest are its first stage, the ends
+// of 64 half steps and the output.
 struct FgWide {
     static constexpr int kSide = 256, kW = 256 * 128, kStage = 2 * 256 * 128, kSf = 2 * kStage, kLds = kSf + 4 * 1024;
 };
@@ -748,6 +756,8 @@ extern "C" int fp8_gemm(const uint8_t* a_codes, const float* a_sf, int64_t a_sf_
     //   32 x 4096   8.4 10.1 13.3 15.0 24.3 48    256 x 4096    -  10.9 13.8 15.4 25.2 49    512 x 4096    -  20.7 14.9 16.7 26.0 50
     //  768 x 4096    -  29.4 26.3 22.2 26.8 50   1024 x 4096    -  39.4 28.8 25.4 27.6 50   1280 x 4096    -  49.0 40.0 36.1 32.6 50
     // 2048 x 4096    -  74.9 55.9 49.7 38.8 52   3000 x 4096    -   111 83.8 72.9 60.9 55   8192 x 8192    -   555  421  362  287 245
+    // 4096 x 4096    -   145  108 91.3 73.9 62   4096 x 4352    -   154  118 99.8 86.0 105  4096 x 5120    -   179  133  115 92.8 105
+    // (the last two's 272 and 320 blocks of 256 x 256 are a second round of a few: the rule does not look at it)
     // Few blocks of K do not pay for a second group's sums: 64 x 64 with two groups and with one (stages of two blocks)
     // 64 x 2048 x 1024 5.0 and 4.5, 33 x 4096 x 2048 6.5 and 6.0, 64 x 8192 x 4096 10.3 and 13.7
     if (T <= 16 && N <= 8192) return launch_fp8_skinny<1>(a, s);

@@ -299,7 +299,9 @@ __device__ __forceinline__ void gg_store(uint8_t* out, int64_t stride, bool vec,
 // The same of fp32, straight from the accumulators: there a lane holds one
 // column of 4 consecutive rows at a time, so that 32 lanes store a row's whole cache
 // line (or part of it, at any stride). Weight gradient of 128 experts x 4096 x 1536,
-// 256 rows each: 892 -> 813 us.
+// 256 rows each: 892 -> 814 us. With ADD each step of 4 rows reads, waits, adds and
+// stores in turn, and there is one block a CU to do it: 2529 us, where the bytes alone
+// are 1.4 ms.
 template <int NT, bool ADD>
 __device__ __forceinline__ void gg_store32(uint8_t* out, int64_t stride, const gg_f16v (&acc)[NT], int live, int left, int cols, int lane) {
     const int c = lane & 31, g = lane >> 5;
@@ -334,13 +336,13 @@ __device__ __forceinline__ void gg_store32(uint8_t* out, int64_t stride, const g
 // tiles' rows dealt round the waves, so that a block of few rows is few tiles of
 // every wave's.
 //
-// What bounds it: 128 experts x 4096 x 1536, 4096 tokens top-8, in 492 us forward is
-// 4.0 TB/s of the 1.98 GB that have to move (a large copy reaches 4.8) at 0.84
-// PFLOP/s; 8 experts of 4096 rows each in 350, 1.18 PFLOP/s (a large library product
+// What bounds it: 128 experts x 4096 x 1536, 4096 tokens top-8, in 495 us forward is
+// 4.0 TB/s of the 1.98 GB that have to move (a large copy reaches 4.8) at 0.83
+// PFLOP/s; 8 experts of 4096 rows each in 365 to 370, 1.12 PFLOP/s (a large library product
 // 1.45). A stage's copies take 0.6 to 1 us to arrive, and the bytes in flight are what
 // LDS holds: hence large blocks, one a CU, and a ring that takes all of it. The 64
-// rows of 8 tokens, 64 x 1536 x 2048, read their experts' 254 MB of weights in 48 us,
-// 5.3 TB/s.
+// rows of 8 tokens, 64 x 1536 x 2048, read their experts' 254 MB of weights in 47 us,
+// 5.4 TB/s.
 enum GgKind { kGgRows, kGgRowsT, kGgWeight };       // forward, input gradient, weight gradient
 
 template <int KIND, int WM, int MW, int NW, bool F32, bool ADD>
@@ -410,8 +412,9 @@ __device__ __forceinline__ void gg_block(const GgArgs& a, const GgBlock& b, uint
         using R = typename S::template Ring<LIVE>;
         constexpr int kAll = R::kAll;
         // Rows whose length is a multiple of some KB meet in few memory channels at one place along them: forward, where both
-        // operands are read along their rows, blocks begin at different stages and go round (D = 2048: 8 tokens' rows 57 ->
-        // 48 us, 128 rows an expert 107 -> 98; 1536, 256 rows: 497 -> 489), by expert and columns. The gradients gain nothing by it.
+        // operands are read along their rows, blocks begin at different stages and go round, by expert and columns (us; 64 x
+        // 1536 x 2048: 8 tokens' rows 53 to 57 -> 47, 16 rows an expert 78 to 84 -> 71, 128 rows 90 -> 86; 128 x 4096 x 1536, 256
+        // rows each 460 -> 445, routed 486 to 497 -> 486). The gradients gain nothing by it.
         const int start = KIND == kGgRows && stages > 0 ? (int)((unsigned)(b.e * nt + n0 / S::kBN) % (unsigned)stages) : 0;
         auto copy = [&](int s, int q0, int q1) __attribute__((always_inline)) {        // copies [q0, q1) of stage s
             const uint32_t at = lds0 + (s % R::kRing) * R::kStage;
@@ -590,16 +593,19 @@ static bool gg_filled(int64_t blocks) { return blocks >= 1024 || 10 * blocks >= 
 // read less per product, from the L2 and of the weights; but a CU without one
 // idles, and where an expert has few rows a block is mostly empty (its empty row
 // tiles are not computed). rows_max counts padding and routes that went elsewhere:
-// the experts' rows are only guessed from it. us, blocks of 256 x 256, 128 x 128
-// and 32 x 128, forward and input gradient:
+// the experts' rows are only guessed from it. us, blocks of 256 x 256 (with tall ones),
+// 128 x 128 and 32 x 128, forward and input gradient, every expert of the same rows:
 //   E x N x D        rows each
-//   128 x 4096 x 1536  256   536 493   628 583   1149 1045     8 x 4096 x 1536   4096   376 354   443 434   909 858
-//   128 x 4096 x 1536  128   345 324   423 421    679  618   128 x 4096 x 1536     32   294 289   307 307   334 326
-//    64 x 1536 x 2048  128    98  92   112 115    168  170    64 x 1536 x 2048     64    85  79    83  86   110 111
-//    64 x 1536 x 2048   16    77  75    72  78     72   77     8 x 1536 x 2048    256    41  36    21  18    31  32
-//     8 x 1536 x 2048   64    23  22    15  16     14   13     1 x 4096 x 4096   1024    74  81    37  38    65  73
-//     1 x 4096 x 4096  256    72  77    31  32     23   25   128 x 4096 x 1536      4   132 145   120 134   116 129
-// (the last in the mean, skewed)
+//   128 x 4096 x 1536  256   450 422   567 518   1080 977     8 x 4096 x 1536   4096   370 348   439 422   876 850
+//   128 x 4096 x 1536  128   336 311   385 360    626 554   128 x 4096 x 1536     32   289 287   297 304   295 304
+//    64 x 1536 x 2048  128    92  86    85  89    143 150    64 x 1536 x 2048     64    81  76    76  79    95  97
+//    64 x 1536 x 2048   16    77  74    72  75     72  75     8 x 1536 x 2048    256    40  35    19  18    29  31
+//     8 x 1536 x 2048   64    22  21    15  16     13  12     1 x 4096 x 4096   1024    72  79    39  40    65  72
+//     1 x 4096 x 4096  256    71  78    31  32     22  23   128 x 4096 x 1536      4   129 142   115 130   113 128
+// (the last in the mean, skewed). Rows of fp32 take 0 to 6% more, in the same order. 256
+// rows in the mean of a routing, 128 x 4096 x 1536: 496 485, 614 586, 1133 1040. Not seen
+// by the rule: how much of rows_max is padding (512 routes over 128 experts in tiles of
+// 128 rows count as 16768 rows, and take the wide blocks: 4 rows each, the last line).
 static int gg_rows_blocks(int64_t rows_max, int E, int cols) {
     const auto blocks = [&](int64_t side) {         // about: half a block of rows is lost an expert
         const int64_t rows = rows_max / side + (rows_max < E ? rows_max : E) / 2, least = rows_max < E ? rows_max : E;
@@ -683,11 +689,13 @@ extern "C" int moe_grouped_gemm_wgrad(const uint16_t* d_out, int64_t d_out_row_s
     a.offsets = expert_offsets; a.counts = expert_counts; a.E = E; a.R = rows_max; a.M = N; a.N = D;
     a.out = (uint8_t*)d_w; a.out_stride = (int64_t)D * (f32 ? 4 : 2); a.out_group = a.out_stride * N; a.out_vec = a.out_stride % 16 == 0;
     // us, blocks of 256 x 256 and 128 x 128, bf16 d_w and fp32:
-    //   128 x 4096 x 1536, rows each 256   690 777   813 1050      64 x 1536 x 2048, 128   136 132   159 145
-    //                                128   527 619   660  763                         64   115 110   145 124
-    //                                 32   383 388   590  567                         16   102 100   132 122
-    //                  4 in the mean, skewed 333 303 586  562       8 x 1536 x 2048, 256    27  23    31  26
-    //     8 x 4096 x 1536,          4096   348 444   355  459       1 x 4096 x 4096, 1024   36  39    41  43
+    //   128 x 4096 x 1536, rows each 256   672 762   814 1033      64 x 1536 x 2048, 128   121 122   148 145
+    //                                128   512 590   637  695                         64   104 102   139 122
+    //                                 32   389 388   584  569                         16   102  99   133 127
+    //                  4 in the mean, skewed 328 310 591  564       8 x 1536 x 2048, 256    27  23    30  26
+    //     8 x 4096 x 1536,          4096   345 443   354  455       1 x 4096 x 4096, 1024   35  40    40  41
+    // Accumulating: 128 x 4096 x 1536, 256 997 944 2529 2538, 32 784 696 2372 2385; 8 x 4096 x 1536, 4096 368 453 449 496 (the
+    // rule has no term for it, though bf16 sums onto many experts' weights are quicker in the smaller blocks)
     // (a block of few rows is its output alone, which the smaller ones write beside another's reads; not so in long runs)
     const int64_t wide = (int64_t)E * ((N + 255) / 256) * ((D + 255) / 256);
     if (rows_max >= (wide >= 4096 ? 96 : 192) * (int64_t)E && wide >= 200 && gg_filled(wide))

@@ -5,9 +5,9 @@
 // g and u are the first and second half of a row of gate_up.
 //
 // Both are HBM-bound and move each byte once: a thread owns 16 bytes of g, u
-// and y. 40704 rows of 1536 (32768 of them tokens'), bf16: the gradient 95 to 102 us,
-// 5.0 to 5.3 TB/s of the 503 MB of the tokens' rows (a large copy 4.8); 64 tokens'
-// rows forward 4.0 us, a launch. Padding rows below total_rows are written as zeros without being read,
+// and y. 40704 rows of 1536 (32768 of them tokens'), bf16: the gradient 96 to 109 us,
+// 4.6 to 5.2 TB/s of the 503 MB of the tokens' rows (a large copy 4.8); 64 tokens'
+// rows forward 4.0 to 4.4 us, a launch. Padding rows below total_rows are written as zeros without being read,
 // rows behind are left.
 #include "common.hpp"
 
